@@ -1,0 +1,565 @@
+// Dense linear layer with a fused epilogue, for the layers of a block that
+// stay at 16 or 8 bits:
+//
+//   Y = residual + gate * act(s_a s_w (A W^T) + bias)
+//
+// A [M x K] activations, W [N x K] weights (both K-major), one operand type:
+// bf16, fp16, E4M3 or INT8; fp32 accumulation (int32 for INT8); Y, bias, gate
+// and residual bf16 or fp16.
+//
+// The tensor cores compute the transposed tile: the MMA's M side is 128
+// features (256 over a pair of SMs), its N side the tokens.  An accumulator
+// lane is then one feature, so the bias and the weight scale are one register
+// per thread, a warp's loads and stores of a token's row cover 32 consecutive
+// features for any alignment and row stride, and a call with few tokens pads
+// them to 16 and not to 128.
+//
+// All operand types go through one pipeline that counts in bytes: a k-block is
+// 128 bytes of a row (64 16-bit or 128 8-bit elements) in the 128-byte
+// swizzle, and one MMA consumes 32 bytes.  The tensor maps zero-fill rows
+// beyond M and N and elements beyond K.
+#pragma once
+
+#include "kg_common.cuh"
+#include "krms8.cuh"
+
+namespace svdq {
+
+enum : int { DK_F16 = 0, DK_E4M3 = 1, DK_INT8 = 2 };       // operand kinds
+enum : int { DENSE_NONE = 0, DENSE_GELU = 1, DENSE_SILU = 2 };
+
+struct DenseParams {
+  uint16_t* y;
+  const uint16_t* bias;   // [N] or null
+  const uint16_t* gate;   // [ceil(M / gate_rows) x N] or null
+  const uint16_t* res;    // [M x N] or null
+  const float* sa;        // [M] or null
+  const float* sw;        // [N] or null
+  int64_t ldy, ldr, ldg;  // elements
+  int gate_rows;
+  int M, N;
+  int kblk;               // 128-byte k-blocks
+  int num_f, num_t;       // feature and token tiles
+  int act;
+  int* err;               // or null
+  uint64_t timeout_ns;
+};
+
+__device__ int g_dense_err;  // error word of calls that pass none
+
+__host__ __device__ constexpr uint32_t idesc_dense(int kind, int out, int M, int N) {
+  // D format f32 / s32; operand format bf16 (1) or fp16 (0), E4M3 (0), S8 (1)
+  const uint32_t d = kind == DK_INT8 ? 2u : 1u;
+  const uint32_t f = kind == DK_INT8 ? 1u : kind == DK_E4M3 ? 0u : out == DT_BF16 ? 1u : 0u;
+  return (d << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+#define SVDQ_DENSE_MMA(GROUP, KIND)                                                             \
+  asm volatile(                                                                                 \
+      "{\n\t.reg .pred p;\n\t"                                                                  \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                               \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d),     \
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)                                               \
+      : "memory")
+
+template <int KIND, bool PAIR>
+__device__ __forceinline__ void dense_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (PAIR) {
+    if constexpr (KIND == DK_F16) SVDQ_DENSE_MMA("2", "f16");
+    else if constexpr (KIND == DK_E4M3) SVDQ_DENSE_MMA("2", "f8f6f4");
+    else SVDQ_DENSE_MMA("2", "i8");
+  } else {
+    if constexpr (KIND == DK_F16) SVDQ_DENSE_MMA("1", "f16");
+    else if constexpr (KIND == DK_E4M3) SVDQ_DENSE_MMA("1", "f8f6f4");
+    else SVDQ_DENSE_MMA("1", "i8");
+  }
+}
+#undef SVDQ_DENSE_MMA
+
+// ------------------------------------------------------------------ epilogue
+// What a lane keeps of its feature n for a whole tile.
+struct DenseLane {
+  bool on;        // n < N
+  float sw, bias;
+};
+
+template <int OUT>
+__device__ __forceinline__ DenseLane dense_lane(const DenseParams& p, int n) {
+  DenseLane l;
+  l.on = n < p.N;
+  l.sw = l.on && p.sw ? __ldg(p.sw + n) : 1.f;
+  l.bias = l.on && p.bias ? to_f32<OUT>(__ldg(p.bias + n)) : 0.f;
+  return l;
+}
+
+// SiLU of two values: x / (1 + 2^(-x log2 e)), with the same approximate
+// exponential and reciprocal as the GELU.
+__device__ __forceinline__ uint64_t silu2(uint64_t x) {
+  const uint64_t a = f2_mul(x, f2_pack(-1.44269504089f, -1.44269504089f));
+  float e0, e1, r0, r1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(f2_lo(a)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(f2_hi(a)));
+  const uint64_t d = f2_add(f2_pack(e0, e1), f2_pack(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(f2_lo(d)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(f2_hi(d)));
+  return f2_mul(x, f2_pack(r0, r1));
+}
+
+// The residual of NC tokens m0 .. of feature n; rows beyond M give 0.
+template <int OUT, int NC>
+__device__ __forceinline__ void dense_residual(const DenseParams& p, const DenseLane& l, int m0, int n, uint16_t* r) {
+  const uint16_t* src = p.res + static_cast<int64_t>(m0) * p.ldr + n;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    r[j] = l.on && m0 + j < p.M ? *src : static_cast<uint16_t>(0);
+    src += p.ldr;
+  }
+}
+
+// NC accumulator columns (tokens m0 ..) of feature n -> Y.
+template <int KIND, int OUT, int NC>
+__device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLane& l, int m0, int n,
+                                            const uint32_t* acc, const uint16_t* r) {
+  float v[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    v[j] = KIND == DK_INT8 ? static_cast<float>(static_cast<int>(acc[j])) : __uint_as_float(acc[j]);
+  if constexpr (KIND != DK_F16) {
+    if (p.sa) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) v[j] *= l.sw * (m0 + j < p.M ? __ldg(p.sa + m0 + j) : 0.f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) v[j] *= l.sw;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) v[j] += l.bias;
+  if (p.act == DENSE_GELU) {
+    gelu_tanh_pairs<NC / 2>(v);
+  } else if (p.act == DENSE_SILU) {
+#pragma unroll
+    for (int j = 0; j < NC; j += 2) {
+      const uint64_t s = silu2(f2_pack(v[j], v[j + 1]));
+      v[j] = f2_lo(s);
+      v[j + 1] = f2_hi(s);
+    }
+  }
+  if (p.gate && l.on) {
+    int g = m0 / p.gate_rows, left = (g + 1) * p.gate_rows - m0;  // tokens left of this gate row
+    const uint16_t* src = p.gate + static_cast<int64_t>(g) * p.ldg + n;
+    float gv = m0 < p.M ? to_f32<OUT>(__ldg(src)) : 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if (left == 0) {
+        left = p.gate_rows;
+        src += p.ldg;
+        if (m0 + j < p.M) gv = to_f32<OUT>(__ldg(src));
+      }
+      --left;
+      v[j] *= gv;
+    }
+  }
+  if (p.res) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] += to_f32<OUT>(r[j]);
+  }
+  uint16_t* dst = p.y + static_cast<int64_t>(m0) * p.ldy + n;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    if (l.on && m0 + j < p.M) *dst = from_f32<OUT>(v[j]);
+    dst += p.ldy;
+  }
+}
+
+// ------------------------------------------------ pairs of SMs, large calls
+// A cluster of two CTAs owns 256 features x BN tokens: rank r loads weight
+// rows [128 r, 128 r + 128) and token rows [BN/2 r, BN/2 r + BN/2) of the
+// tile, the leader issues the pair's MMAs (M = 256), and each SM accumulates
+// its 128 features x BN tokens.  Persistent over tiles; two accumulators in
+// tensor memory, so the epilogue of one tile runs under the MMAs of the next.
+// Warps: 0 TMA, 1 MMA and tensor memory, 2-3 idle, 4-11 epilogue.
+constexpr int DP_THREADS = 384;
+constexpr int DP_EPI_WARPS = 8;
+
+template <int BN>
+struct DensePairSmem {
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int A_BYTES = BN / 2 * 128;
+  static constexpr int STAGE = W_BYTES + A_BYTES;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr uint32_t TX = 2 * STAGE;
+  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int TOTAL = BAR_OFF + 256 + 1024;
+  static_assert(TOTAL <= 232448, "shared memory per CTA");
+};
+
+// Tiles in bands of kDenseBand token tiles, features outermost inside a band:
+// the tiles that run at one time share few weight and token blocks.
+constexpr int kDenseBand = 8;
+__device__ __forceinline__ void dense_tile(const DenseParams& p, int tile, int& ft, int& tt) {
+  const int band = tile / (kDenseBand * p.num_f);
+  const int in = tile - band * kDenseBand * p.num_f;
+  const int wide = min(kDenseBand, p.num_t - band * kDenseBand);
+  ft = in / wide;
+  tt = band * kDenseBand + in - ft * wide;
+}
+
+template <int KIND, int OUT, int BN>
+__global__ void __launch_bounds__(DP_THREADS, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                      const __grid_constant__ DenseParams p) {
+  using S = DensePairSmem<BN>;
+  constexpr int NST = S::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);
+  const uint32_t bar_full = smem_u32(bars);
+  const uint32_t bar_empty = smem_u32(bars + NST);
+  const uint32_t bar_acc_full = smem_u32(bars + 2 * NST);       // two
+  const uint32_t bar_acc_empty = smem_u32(bars + 2 * NST + 2);  // two, the leader's count
+  const uint32_t bar_drain = smem_u32(bars + 2 * NST + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int cid = static_cast<int>(blockIdx.x >> 1);
+  const int nclu = static_cast<int>(gridDim.x >> 1);
+  const Guard guard{p.err ? p.err : &g_dense_err, abort_flag, p.timeout_ns};
+  const int num_tiles = p.num_f * p.num_t;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_acc_full + 8 * i, 1);
+      mbar_init(bar_acc_empty + 8 * i, 2 * DP_EPI_WARPS);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs initialised, tensor memory allocated
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();  // operands and outputs may belong to the previous kernel of the stream
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_w);
+      tma_prefetch_desc(&tm_a);
+      const uint32_t full0 = mapa_shared(bar_full, 0);  // the leader's full barriers
+      int s = 0;
+      uint32_t ph = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int tile = cid; tile < num_tiles && ok; tile += nclu) {
+        int ft, tt;
+        dense_tile(p, tile, ft, tt);
+        const int wrow = ft * 256 + static_cast<int>(rank) * 128;
+        const int arow = tt * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = 0; kb < p.kblk; ++kb) {
+          if (!(ok = wait_bounded(bar_empty + 8 * s, ph ^ 1, guard, 0x301))) break;
+          issued &= ~(1u << s);
+          const uint32_t st = sbase + s * S::STAGE;
+          if (rank == 0) mbar_expect_tx(bar_full + 8 * s, S::TX);
+          // whole boxes always: what lies beyond N, M or K is zero-filled
+          const int kc = kb * (KIND == DK_F16 ? 64 : 128);
+          tma_load_2d_pair(st, &tm_w, full0 + 8 * s, kc, wrow);
+          tma_load_2d_pair(st + S::W_BYTES, &tm_a, full0 + 8 * s, kc, arow);
+          issued |= 1u << s;
+          issued_par = (issued_par & ~(1u << s)) | (ph << s);
+          if (++s == NST) { s = 0; ph ^= 1; }
+        }
+      }
+      if (*abort_flag && rank == 0) drain_loads(bar_full, issued, issued_par, NST, p.timeout_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id = idesc_dense(KIND, OUT, 256, BN);
+      const uint64_t dW0 = smem_desc(sbase, 16, 1024, SWZ_128B);
+      const uint64_t dA0 = smem_desc(sbase + S::W_BYTES, 16, 1024, SWZ_128B);
+      constexpr uint64_t kStage = S::STAGE >> 4;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = cid, j = 0; tile < num_tiles && ok; tile += nclu, ++j) {
+        const int ac = j & 1;
+        const uint32_t d = tmem + ac * 256;
+        if (j > 1 && !(ok = wait_bounded_cl(bar_acc_empty + 8 * ac, ((j >> 1) - 1) & 1, guard, 0x302))) break;
+        tc_fence_after();
+        for (int kb = 0; kb < p.kblk; ++kb) {
+          if (!(ok = wait_bounded(bar_full + 8 * s, ph, guard, 0x303))) break;
+          tc_fence_after();
+          const uint64_t so = kStage * s;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dense_mma<KIND, true>(d, dW0 + so + 2 * i, dA0 + so + 2 * i, id, (kb | i) != 0);
+          tc_commit_pair(bar_empty + 8 * s, 0x3);
+          if (++s == NST) { s = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        tc_commit_pair(bar_acc_full + 8 * ac, 0x3);
+      }
+      // every MMA of the pair has completed before either CTA frees tensor memory
+      tc_commit_pair(bar_drain, 0x1);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bar_drain, 0) && global_timer_ns() - t0 < p.timeout_ns) {
+      }
+    }
+  } else if (warp >= 4) {
+    const int e = warp - 4;
+    const int q = warp & 3;              // tensor-memory lane group of this warp
+    const int c0 = (e >> 2) * (BN / 2);  // its half of the tokens
+    const uint32_t acc_empty0 = mapa_shared(bar_acc_empty, 0);
+    for (int tile = cid, j = 0; tile < num_tiles; tile += nclu, ++j) {
+      int ft, tt;
+      dense_tile(p, tile, ft, tt);
+      const int ac = j & 1;
+      const int n = ft * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int m0 = tt * BN + c0;
+      const DenseLane l = dense_lane<OUT>(p, n);
+      uint16_t r[2][16];
+      if (p.res) dense_residual<OUT, 16>(p, l, m0, n, r[0]);
+      if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
+      tc_fence_after();
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + ac * 256 + c0;
+#pragma unroll 1
+      for (int cc = 0; cc < BN / 2; cc += 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = cc + 16 * h;
+          uint32_t v[16];
+          tmem_ld_x16(ta + c, v);
+          // the next columns' residual is on its way while these are stored
+          if (p.res && c + 16 < BN / 2) dense_residual<OUT, 16>(p, l, m0 + c + 16, n, r[1 - h]);
+          tmem_ld_wait();
+          if (c + 16 == BN / 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * ac);
+          }
+          if (m0 + c < p.M) dense_store<KIND, OUT, 16>(p, l, m0 + c, n, v, r[h]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();  // the pair's MMAs, loads and remote arrivals are all done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// -------------------------------------------- single SMs, few tokens or tiles
+// One CTA per (128 features x BN tokens, slice of K).  A cluster of `split`
+// CTAs shares a tile's K range; their partial sums meet in distributed shared
+// memory, each CTA adds up and stores its share of the tokens, in rank order,
+// so the result does not depend on timing and needs no workspace.
+// Warps: 0 TMA, 1 MMA and tensor memory, 2-5 epilogue.
+constexpr int DS_THREADS = 192;
+
+template <int BN>
+struct DenseSoloSmem {
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int A_BYTES = BN * 128;
+  static constexpr int STAGE = W_BYTES + A_BYTES;
+  static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 3;  // two CTAs fit an SM
+  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int TOTAL = BAR_OFF + 256 + 1024;
+  static_assert(128 * BN * 4 <= BAR_OFF, "the partial tile fits the stages");
+  static_assert(2 * TOTAL <= 232448, "shared memory of two CTAs");
+};
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int KIND, int OUT, int BN>
+__global__ void __launch_bounds__(DS_THREADS, 2)
+    dense_solo_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                      const __grid_constant__ DenseParams p, int split) {
+  using S = DenseSoloSmem<BN>;
+  constexpr int NST = S::STAGES;
+  constexpr int COLS = BN < 32 ? 32 : BN;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);
+  const uint32_t bar_full = smem_u32(bars);
+  const uint32_t bar_empty = smem_u32(bars + NST);
+  const uint32_t bar_acc = smem_u32(bars + 2 * NST);
+  const uint32_t bar_drain = smem_u32(bars + 2 * NST + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(blockIdx.x) % split;
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int ft = tile % p.num_f, tt = tile / p.num_f;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblk) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblk) * (rank + 1) / split);
+  const Guard guard{p.err ? p.err : &g_dense_err, abort_flag, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    mbar_init(bar_acc, 1);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_w);
+      tma_prefetch_desc(&tm_a);
+      int s = 0;
+      uint32_t ph = 0, issued = 0, issued_par = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bounded(bar_empty + 8 * s, ph ^ 1, guard, 0x311)) break;
+        issued &= ~(1u << s);
+        const uint32_t st = sbase + s * S::STAGE;
+        mbar_expect_tx(bar_full + 8 * s, S::STAGE);
+        const int kc = kb * (KIND == DK_F16 ? 64 : 128);
+        tma_load_2d(st, &tm_w, bar_full + 8 * s, kc, ft * 128);
+        tma_load_2d(st + S::W_BYTES, &tm_a, bar_full + 8 * s, kc, tt * BN);
+        issued |= 1u << s;
+        issued_par = (issued_par & ~(1u << s)) | (ph << s);
+        if (++s == NST) { s = 0; ph ^= 1; }
+      }
+      if (*abort_flag) drain_loads(bar_full, issued, issued_par, NST, p.timeout_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_dense(KIND, OUT, 128, BN);
+      const uint64_t dW0 = smem_desc(sbase, 16, 1024, SWZ_128B);
+      const uint64_t dA0 = smem_desc(sbase + S::W_BYTES, 16, 1024, SWZ_128B);
+      constexpr uint64_t kStage = S::STAGE >> 4;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!(ok = wait_bounded(bar_full + 8 * s, ph, guard, 0x312))) break;
+        tc_fence_after();
+        const uint64_t so = kStage * s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dense_mma<KIND, false>(tmem, dW0 + so + 2 * i, dA0 + so + 2 * i, id, (kb != kb0) | (i != 0));
+        tc_commit(bar_empty + 8 * s);
+        if (++s == NST) { s = 0; ph ^= 1; }
+      }
+      if (ok) tc_commit(bar_acc);
+      tc_commit(bar_drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bar_drain, 0) && global_timer_ns() - t0 < p.timeout_ns) {
+      }
+    }
+  }
+  const int q = warp & 3;
+  const int f = q * 32 + lane;          // feature of the tile
+  const int n = ft * 128 + f;
+  const int m0 = tt * BN;
+  const int valid = min(BN, p.M - m0);  // tokens of the tile
+  bool ok = true;
+  DenseLane l = {};
+  if (warp >= 2) {
+    l = dense_lane<OUT>(p, n);
+    ok = __all_sync(0xffffffffu, wait_bounded(bar_acc, 0, guard, 0x313, 32));
+    tc_fence_after();
+    const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    if (split == 1) {
+      if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < valid; c += 16) {
+          uint32_t v[16];
+          uint16_t r[16];
+          tmem_ld_x16(ta + c, v);
+          if (p.res) dense_residual<OUT, 16>(p, l, m0 + c, n, r);
+          tmem_ld_wait();
+          dense_store<KIND, OUT, 16>(p, l, m0 + c, n, v, r);
+        }
+      }
+    } else if (ok) {
+      // every stage has been consumed: the partial tile goes into their place
+      uint32_t* part = reinterpret_cast<uint32_t*>(smem);
+#pragma unroll 1
+      for (int c = 0; c < valid; c += 16) {
+        uint32_t v[16];
+        tmem_ld_x16(ta + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + f] = v[j];
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync();  // all partial tiles are in place
+    if (warp >= 2 && ok) {
+      const int per = 2 * ((valid + 2 * split - 1) / (2 * split));  // even: two tokens at a time
+      const int c1 = min(valid, (rank + 1) * per);
+      for (int c = rank * per; c < c1; c += 2) {
+        uint32_t v[2];
+        uint16_t r[2];
+        if (p.res) dense_residual<OUT, 2>(p, l, m0 + c, n, r);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t at = sbase + ((c + j) * 128 + f) * 4;
+          uint32_t x[8];
+#pragma unroll
+          for (int o = 0; o < 8; ++o) x[o] = o < split ? ld_cluster_u32(mapa_shared(at, o)) : 0u;
+          if constexpr (KIND == DK_INT8) {
+            int a = 0;
+#pragma unroll
+            for (int o = 0; o < 8; ++o) a += static_cast<int>(x[o]);
+            v[j] = static_cast<uint32_t>(a);
+          } else {
+            float a = 0.f;
+#pragma unroll
+            for (int o = 0; o < 8; ++o) a += __uint_as_float(x[o]);
+            v[j] = __float_as_uint(a);
+          }
+        }
+        dense_store<KIND, OUT, 2>(p, l, m0 + c, n, v, r);
+      }
+    }
+    cluster_sync();  // no CTA leaves while its partial tile may be read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, COLS);
+  }
+}
+
+}  // namespace svdq

@@ -1,0 +1,510 @@
+// Host side of the operators around the 4-bit layers: the dense linear with a
+// fused epilogue, the RMS norm with an 8-bit output and rotary positions with
+// several axes.  Argument validation, variant choice and launches; the C
+// declarations and their documentation live in include/svdq.h.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <utility>
+
+#include "host_common.cuh"
+#include "kdense.cuh"
+#include "krms8.cuh"
+#include "krope_axes.cuh"
+
+using namespace svdq;
+
+struct svdq_rope {
+  RopePlan plan;
+  int axes;
+};
+
+namespace {
+
+struct DeviceInfo {
+  int dev = 0, sms = 0;
+};
+
+// check_device() of the current device, asked once per device ordinal.
+svdq_status device_info(DeviceInfo* d) {
+  static std::atomic<int> known[64];  // SM count of a usable device
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
+    if (const int sms = known[dev].load(std::memory_order_acquire); sms > 0) {
+      d->dev = dev;
+      d->sms = sms;
+      return SVDQ_OK;
+    }
+  } else {
+    cudaGetLastError();
+  }
+  if (svdq_status s = check_device(&d->dev, &d->sms); s != SVDQ_OK) return s;
+  if (d->dev < 64) known[d->dev].store(d->sms, std::memory_order_release);
+  return SVDQ_OK;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int dtype_size(int t) { return t == SVDQ_FP32 ? 4 : t == SVDQ_BF16 || t == SVDQ_FP16 ? 2 : 1; }
+
+// `rows` rows of `width` bytes, `ld` bytes apart.
+struct Region {
+  const void* p;
+  int64_t rows, width, ld;
+  uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }
+  uintptr_t hi() const { return lo() + static_cast<uintptr_t>((rows - 1) * ld + width); }
+};
+
+// Whether two regions share bytes.  Column ranges of one buffer (the same row
+// distance) that do not meet are apart although their spans interleave.
+bool overlap(const Region& a, const Region& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1) return false;
+  if (a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
+  if (a.ld == b.ld && a.ld > 0) {
+    const Region& l = a.lo() <= b.lo() ? a : b;
+    const Region& h = a.lo() <= b.lo() ? b : a;
+    const int64_t o = static_cast<int64_t>((h.lo() - l.lo()) % static_cast<uintptr_t>(a.ld));
+    if (l.width <= o && o + h.width <= a.ld) return false;
+  }
+  return true;
+}
+bool same(const Region& a, const Region& b) { return a.p == b.p && (a.ld == b.ld || a.rows == 1); }
+
+// ------------------------------------------------------------------ RMS norm
+template <int DT, int VEC, int CH>
+svdq_status launch_rms_t(const RmsParams& p, int64_t M, int nt, cudaStream_t st) {
+  LaunchCfg lc(dim3(static_cast<unsigned>(M)), dim3(nt), 0, st);
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_kernel<DT, VEC, CH>, p));
+  return SVDQ_OK;
+}
+
+template <int DT, int VEC>
+svdq_status launch_rms_v(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
+  const int64_t pieces = cdiv(p.K, VEC);
+  // pieces a thread: one where a few rows have the device to themselves
+  // (latency), else two to four, for loads in flight and fewer warps to join
+  const int64_t want = M <= 2 * sms ? 1 : pieces <= 256 ? 2 : 4;
+  const int64_t ch = std::max(want, cdiv(pieces, 1024));
+  auto threads = [&](int c) { return static_cast<int>(cdiv(cdiv(pieces, c), 32) * 32); };
+  if (ch <= 1) return launch_rms_t<DT, VEC, 1>(p, M, threads(1), st);
+  if (ch <= 2) return launch_rms_t<DT, VEC, 2>(p, M, threads(2), st);
+  if (ch <= 4) return launch_rms_t<DT, VEC, 4>(p, M, threads(4), st);
+  if constexpr (VEC <= 4) {
+    if (ch <= 8) return launch_rms_t<DT, VEC, 8>(p, M, threads(8), st);
+  }
+  if constexpr (VEC == 1) {
+    if (ch <= 32) return launch_rms_t<DT, VEC, 32>(p, M, threads(32), st);
+  }
+  return SVDQ_ERR_SHAPE;
+}
+
+template <int DT>
+svdq_status launch_rms(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
+  constexpr int V = DT == DT_FP32 ? 4 : 8;
+  const bool vec = p.K % V == 0 && aligned16(p.x) && p.ldx % V == 0 && (!p.res || (aligned16(p.res) && p.ldr % V == 0)) &&
+                   (!p.h || (aligned16(p.h) && p.ldh % V == 0)) && (!p.w || (aligned16(p.w) && p.ldw % V == 0)) &&
+                   aligned(p.codes, V) && p.ldc % V == 0;
+  return vec ? launch_rms_v<DT, V>(p, M, sms, st) : launch_rms_v<DT, 1>(p, M, sms, st);
+}
+
+// --------------------------------------------------------------------- rotary
+template <int DT, int VEC>
+svdq_status launch_rope_v(const RopeParams& p, cudaStream_t st) {
+  LaunchCfg lc(dim3(static_cast<unsigned>(cdiv(p.tokens, ROPE_TOKENS))), dim3(ROPE_THREADS), 0, st);
+  SVDQ_TRY(p.plan.interleaved ? cudaLaunchKernelEx(&lc.cfg, rope_axes_kernel<DT, VEC, true>, p)
+                              : cudaLaunchKernelEx(&lc.cfg, rope_axes_kernel<DT, VEC, false>, p));
+  return SVDQ_OK;
+}
+
+template <int DT>
+svdq_status launch_rope(const RopeParams& p, cudaStream_t st) {
+  constexpr int V = DT == DT_FP32 ? 4 : 8;
+  const int R = 2 * p.plan.pairs;
+  bool vec = (p.plan.interleaved ? R : R / 2) % V == 0 && (p.plan.D - R) % V == 0;
+  for (const RopeTensor& t : p.t)
+    vec = vec && (t.heads == 0 || (aligned16(t.x) && aligned16(t.out) && t.xb % V == 0 && t.xs % V == 0 &&
+                                   t.xh % V == 0 && t.ob % V == 0 && t.os % V == 0 && t.oh % V == 0));
+  return vec ? launch_rope_v<DT, V>(p, st) : launch_rope_v<DT, 1>(p, st);
+}
+
+svdq_status rope_pos(const svdq_rope_positions* pos, RopePos* out) {
+  if (!pos) return SVDQ_ERR_INVALID_ARG;
+  if (pos->type != SVDQ_POS_INT32 && pos->type != SVDQ_POS_INT64 && pos->type != SVDQ_POS_FP32)
+    return SVDQ_ERR_INVALID_ARG;
+  if (!pos->p) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned(pos->p, pos->type == SVDQ_POS_INT64 ? 8 : 4)) return SVDQ_ERR_ALIGNMENT;
+  if (pos->batch_stride < 0 || pos->token_stride < 0 || pos->axis_stride < 0) return SVDQ_ERR_SHAPE;
+  *out = RopePos{pos->p, static_cast<int>(pos->type), pos->batch_stride, pos->token_stride, pos->axis_stride};
+  return SVDQ_OK;
+}
+
+// The bytes of a [B, S, H, D] tensor with strides: its dimensions by rising
+// stride, n elements each.
+struct Nest {
+  const void* p;
+  int64_t n[3], st[3];  // bytes
+  int64_t row;          // bytes of a head
+  int64_t span(int dims) const {  // of the `dims` innermost dimensions
+    int64_t w = row;
+    for (int i = 0; i < dims; ++i) w += (n[i] - 1) * st[i];
+    return w;
+  }
+};
+Nest nest(const void* p, int64_t B, int64_t S, int64_t H, const int64_t* stride, int64_t D, int es) {
+  Nest t{p, {1, 1, 1}, {0, 0, 0}, D * es};
+  const int64_t n[3] = {B, S, H};
+  int64_t order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int64_t a, int64_t b) {
+    return std::make_pair(n[a] > 1, stride[a]) < std::make_pair(n[b] > 1, stride[b]);
+  });
+  for (int i = 0; i < 3; ++i) {
+    t.n[i] = n[order[i]];
+    t.st[i] = t.n[i] > 1 ? stride[order[i]] * es : 0;
+  }
+  return t;
+}
+// Whether no two heads of the tensor meet.
+bool nests(const Nest& t) {
+  for (int i = 0; i < 3; ++i)
+    if (t.n[i] > 1 && t.st[i] < t.span(i)) return false;
+  return true;
+}
+// Whether two tensors are not known to be apart: neither their spans, nor the
+// column ranges of their outermost dimension, nor (two outermost dimensions
+// that form one) those of the next.
+bool may_meet(const Nest& a, const Nest& b) {
+  if (!a.p || !b.p) return false;
+  if (!overlap(Region{a.p, a.n[2], a.span(2), a.st[2]}, Region{b.p, b.n[2], b.span(2), b.st[2]})) return false;
+  auto merges = [](const Nest& t) { return t.n[2] == 1 || t.st[2] == t.n[1] * t.st[1]; };
+  return !merges(a) || !merges(b) ||
+         overlap(Region{a.p, a.n[1] * a.n[2], a.span(1), a.st[1]}, Region{b.p, b.n[1] * b.n[2], b.span(1), b.st[1]});
+}
+
+constexpr int64_t kRopeMaxTokens = 1ll << 31;
+constexpr int64_t kRopeMaxSpan = 1ll << 44;  // elements of a dimension's extent
+
+// ---------------------------------------------------------------------- dense
+// Clusters of two CTAs that fit on the device at once (cached per device,
+// stored + 1).
+template <int KIND, int OUT, int BN>
+int dense_pair_clusters(const DeviceInfo& d) {
+  static std::atomic<int> cache[64];
+  if (d.dev < 0 || d.dev >= 64) return 0;
+  if (const int known = cache[d.dev].load(std::memory_order_acquire); known > 0) return known - 1;
+  constexpr int smem = DensePairSmem<BN>::TOTAL;
+  if (ensure_smem<dense_pair_kernel<KIND, OUT, BN>>(smem) != SVDQ_OK) return 0;
+  LaunchCfg lc(dim3(2 * (d.sms / 2)), dim3(DP_THREADS), smem, nullptr, 2);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, OUT, BN>, &lc.cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;  // not cached: the next call asks again
+  }
+  cache[d.dev].store(n + 1, std::memory_order_release);
+  return n;
+}
+
+struct DenseCall {
+  const svdq_dense_desc* d;
+  DeviceInfo dev;
+  DenseParams p;
+  cudaStream_t st;
+  int64_t lda, ldw;  // bytes
+};
+
+// Maps of W and A with boxes of 128 bytes x rows.
+template <int KIND, int OUT>
+svdq_status dense_maps(const DenseCall& c, int wrows, int arows, CUtensorMap* tw, CUtensorMap* ta) {
+  constexpr CUtensorMapDataType dt = KIND != DK_F16 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : OUT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  constexpr int es = KIND == DK_F16 ? 2 : 1;
+  if (svdq_status s = make_tmap(tw, c.d->w, dt, es, c.d->K, c.d->N, 128 / es, wrows, CU_TENSOR_MAP_SWIZZLE_128B, c.ldw);
+      s != SVDQ_OK)
+    return s;
+  return make_tmap(ta, c.d->a, dt, es, c.d->K, c.d->M, 128 / es, arows, CU_TENSOR_MAP_SWIZZLE_128B, c.lda);
+}
+
+template <int KIND, int OUT, int BN>
+svdq_status launch_dense_pair(DenseCall& c) {
+  constexpr int smem = DensePairSmem<BN>::TOTAL;
+  const int clusters = dense_pair_clusters<KIND, OUT, BN>(c.dev);
+  if (clusters < 1) return SVDQ_ERR_CUDA;
+  CUtensorMap tw, ta;
+  if (svdq_status s = dense_maps<KIND, OUT>(c, 128, BN / 2, &tw, &ta); s != SVDQ_OK) return s;
+  c.p.num_f = static_cast<int>(cdiv(c.p.N, 256));
+  c.p.num_t = static_cast<int>(cdiv(c.p.M, BN));
+  const int tiles = c.p.num_f * c.p.num_t;
+  LaunchCfg lc(dim3(2 * std::min(tiles, clusters)), dim3(DP_THREADS), smem, c.st, 2);
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_pair_kernel<KIND, OUT, BN>, tw, ta, c.p));
+  return SVDQ_OK;
+}
+
+template <int KIND, int OUT, int BN>
+svdq_status launch_dense_solo(DenseCall& c, int split) {
+  constexpr int smem = DenseSoloSmem<BN>::TOTAL;
+  if (svdq_status s = ensure_smem<dense_solo_kernel<KIND, OUT, BN>>(smem); s != SVDQ_OK) return s;
+  CUtensorMap tw, ta;
+  if (svdq_status s = dense_maps<KIND, OUT>(c, 128, BN, &tw, &ta); s != SVDQ_OK) return s;
+  c.p.num_f = static_cast<int>(cdiv(c.p.N, 128));
+  c.p.num_t = static_cast<int>(cdiv(c.p.M, BN));
+  LaunchCfg lc(dim3(static_cast<unsigned>(split) * c.p.num_f * c.p.num_t), dim3(DS_THREADS), smem, c.st, split);
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_solo_kernel<KIND, OUT, BN>, tw, ta, c.p, split));
+  return SVDQ_OK;
+}
+
+// The variant of a call.
+struct DenseChoice {
+  int pair;   // pairs of SMs
+  int bn;     // tokens per tile
+  int split;  // CTAs that share a tile's K range
+};
+
+DenseChoice dense_choose(int64_t M, int64_t N, int kblk, int sms) {
+  const int64_t nf = cdiv(N, 128);
+  DenseChoice c{0, 16, 1};
+  if (cdiv(N, 256) * cdiv(M, 256) >= sms / 2) return DenseChoice{1, 256, 1};
+  if (cdiv(N, 256) * cdiv(M, 128) >= sms / 2) return DenseChoice{1, 128, 1};
+  while (c.bn < 128 && c.bn < M) c.bn *= 2;
+  while (c.bn > 16 && nf * cdiv(M, c.bn) < sms / 2) c.bn /= 2;
+  while (c.split < 8 && nf * cdiv(M, c.bn) * c.split * 2 <= 2 * sms && kblk >= 4 * c.split) c.split *= 2;
+  return c;
+}
+
+template <int KIND, int OUT>
+svdq_status launch_dense(DenseCall& c) {
+  const DenseChoice v = dense_choose(c.p.M, c.p.N, c.p.kblk, c.dev.sms);
+  if (v.pair) return v.bn == 256 ? launch_dense_pair<KIND, OUT, 256>(c) : launch_dense_pair<KIND, OUT, 128>(c);
+  switch (v.bn) {
+    case 16: return launch_dense_solo<KIND, OUT, 16>(c, v.split);
+    case 32: return launch_dense_solo<KIND, OUT, 32>(c, v.split);
+    case 64: return launch_dense_solo<KIND, OUT, 64>(c, v.split);
+  }
+  return launch_dense_solo<KIND, OUT, 128>(c, v.split);
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
+  if (!d) return SVDQ_ERR_INVALID_ARG;
+  const bool wide = d->in == SVDQ_BF16 || d->in == SVDQ_FP16;
+  if (!wide && d->in != SVDQ_E4M3 && d->in != SVDQ_INT8) return SVDQ_ERR_INVALID_ARG;
+  if (d->out != SVDQ_BF16 && d->out != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
+  if (wide && d->out != d->in) return SVDQ_ERR_INVALID_ARG;
+  if (wide && (d->a_scale || d->w_scale)) return SVDQ_ERR_INVALID_ARG;
+  if (d->act != SVDQ_ACT_NONE && d->act != SVDQ_ACT_GELU && d->act != SVDQ_ACT_SILU) return SVDQ_ERR_INVALID_ARG;
+  const int64_t M = d->M, N = d->N, K = d->K;
+  const int64_t es = wide ? 2 : 1;
+  if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 24) || K < 1 || K > 65536) return SVDQ_ERR_SHAPE;
+  if (cdiv(M, 16) * cdiv(N, 128) > (1 << 27)) return SVDQ_ERR_SHAPE;
+  constexpr int64_t kLdMax = 1ll << 36;
+  if ((M > 1 && (d->lda < K || d->ldy < N)) || (N > 1 && d->ldw < K)) return SVDQ_ERR_SHAPE;
+  if (d->lda > kLdMax || d->ldw > kLdMax || d->ldy > kLdMax) return SVDQ_ERR_SHAPE;
+  if (d->residual && (d->ldr < 0 || d->ldr > kLdMax)) return SVDQ_ERR_SHAPE;
+  if (d->gate && (d->gate_rows < 1 || d->ldg < 0 || d->ldg > kLdMax)) return SVDQ_ERR_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (!d->a || !d->w || !d->y) return SVDQ_ERR_INVALID_ARG;
+  // rows that are read through tensor maps start on 16-byte boundaries
+  if (!aligned16(d->a) || !aligned16(d->w)) return SVDQ_ERR_ALIGNMENT;
+  if ((M > 1 && d->lda * es % 16 != 0) || (N > 1 && d->ldw * es % 16 != 0)) return SVDQ_ERR_ALIGNMENT;
+  if (!aligned(d->y, 2) || !aligned(d->bias, 2) || !aligned(d->gate, 2) || !aligned(d->residual, 2) ||
+      !aligned(d->a_scale, 4) || !aligned(d->w_scale, 4) || !aligned(d->device_error, 4))
+    return SVDQ_ERR_ALIGNMENT;
+  const int64_t gates = d->gate ? cdiv(M, d->gate_rows) : 0;
+  const Region y{d->y, M, 2 * N, 2 * d->ldy};
+  const Region r{d->residual, M, 2 * N, 2 * d->ldr};
+  if (overlap(y, Region{d->a, M, K * es, d->lda * es}) || overlap(y, Region{d->w, N, K * es, d->ldw * es}) ||
+      overlap(y, Region{d->bias, 1, 2 * N, 2 * N}) || overlap(y, Region{d->gate, gates, 2 * N, 2 * d->ldg}) ||
+      overlap(y, Region{d->a_scale, 1, 4 * M, 4 * M}) || overlap(y, Region{d->w_scale, 1, 4 * N, 4 * N}) ||
+      (overlap(y, r) && !same(y, r)))
+    return SVDQ_ERR_INVALID_ARG;
+  DenseCall c;
+  c.d = d;
+  if (svdq_status s = device_info(&c.dev); s != SVDQ_OK) return s;
+  c.st = static_cast<cudaStream_t>(stream);
+  const int64_t packed = cdiv(K * es, 16) * 16;  // row distance of a single row: any
+  c.lda = M > 1 ? d->lda * es : packed;
+  c.ldw = N > 1 ? d->ldw * es : packed;
+  c.p = DenseParams{};
+  c.p.y = static_cast<uint16_t*>(d->y);
+  c.p.bias = static_cast<const uint16_t*>(d->bias);
+  c.p.gate = static_cast<const uint16_t*>(d->gate);
+  c.p.res = static_cast<const uint16_t*>(d->residual);
+  c.p.sa = d->a_scale;
+  c.p.sw = d->w_scale;
+  c.p.ldy = d->ldy;
+  c.p.ldr = d->ldr;
+  c.p.ldg = d->ldg;
+  c.p.gate_rows = static_cast<int>(std::min(d->gate ? d->gate_rows : M, M));
+  c.p.M = static_cast<int>(M);
+  c.p.N = static_cast<int>(N);
+  c.p.kblk = static_cast<int>(cdiv(K * es, 128));
+  c.p.act = static_cast<int>(d->act);
+  c.p.err = d->device_error;
+  c.p.timeout_ns = kDefaultTimeoutNs;
+  const bool bf = d->out == SVDQ_BF16;
+  if (wide) return bf ? launch_dense<DK_F16, DT_BF16>(c) : launch_dense<DK_F16, DT_FP16>(c);
+  if (d->in == SVDQ_E4M3) return bf ? launch_dense<DK_E4M3, DT_BF16>(c) : launch_dense<DK_E4M3, DT_FP16>(c);
+  return bf ? launch_dense<DK_INT8, DT_BF16>(c) : launch_dense<DK_INT8, DT_FP16>(c);
+}
+
+svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
+  if (!d) return SVDQ_ERR_INVALID_ARG;
+  if (d->in != SVDQ_BF16 && d->in != SVDQ_FP16 && d->in != SVDQ_FP32) return SVDQ_ERR_INVALID_ARG;
+  if (d->out != SVDQ_E4M3 && d->out != SVDQ_INT8) return SVDQ_ERR_INVALID_ARG;
+  if (d->norm != 0 && d->norm != 1) return SVDQ_ERR_INVALID_ARG;
+  if (d->norm && !(d->eps > 0.0f && d->eps < 1.0f)) return SVDQ_ERR_INVALID_ARG;
+  const int64_t M = d->M, K = d->K;
+  if (M < 0 || M > INT32_MAX || K < 1 || K > 32768) return SVDQ_ERR_SHAPE;
+  constexpr int64_t kLdMax = 1ll << 28;
+  if (d->ldx < 0 || d->ldx > kLdMax || (d->residual && (d->ldr < 0 || d->ldr > kLdMax))) return SVDQ_ERR_SHAPE;
+  if (M > 1 && (d->ldc < K || (d->h && d->ldh < K))) return SVDQ_ERR_SHAPE;
+  if (d->ldc > kLdMax || (d->h && d->ldh > kLdMax)) return SVDQ_ERR_SHAPE;
+  if (d->weight && (d->weight_rows < 1 || d->ldw < 0 || d->ldw > kLdMax)) return SVDQ_ERR_SHAPE;
+  if (M == 0) return SVDQ_OK;
+  if (!d->x || !d->codes || !d->scales) return SVDQ_ERR_INVALID_ARG;
+  const int es = dtype_size(d->in);
+  if (!aligned(d->x, es) || !aligned(d->residual, es) || !aligned(d->h, es) || !aligned(d->weight, es) ||
+      !aligned(d->scales, 4))
+    return SVDQ_ERR_ALIGNMENT;
+  const Region x{d->x, M, K * es, d->ldx * es}, r{d->residual, M, K * es, d->ldr * es};
+  const Region h{d->h, M, K * es, d->ldh * es}, c{d->codes, M, K, d->ldc};
+  const Region s{d->scales, 1, 4 * M, 4 * M};
+  const Region w{d->weight, d->weight ? cdiv(M, d->weight_rows) : 0, K * es, d->ldw * es};
+  if ((overlap(h, x) && !same(h, x)) || (overlap(h, r) && !same(h, r)) || overlap(h, w) || overlap(h, c) ||
+      overlap(h, s) || overlap(c, x) || overlap(c, r) || overlap(c, w) || overlap(c, s) || overlap(s, x) ||
+      overlap(s, r) || overlap(s, w))
+    return SVDQ_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (svdq_status e = device_info(&dev); e != SVDQ_OK) return e;
+  RmsParams p{};
+  p.x = d->x;
+  p.res = d->residual;
+  p.h = d->h;
+  p.w = d->weight;
+  p.codes = static_cast<uint8_t*>(d->codes);
+  p.scales = d->scales;
+  p.ldx = d->ldx;
+  p.ldr = d->ldr;
+  p.ldh = d->ldh;
+  p.ldw = d->ldw;
+  p.ldc = d->ldc;
+  p.w_rows = d->weight ? d->weight_rows : 1;
+  p.K = static_cast<int>(K);
+  p.norm = d->norm;
+  p.int8 = d->out == SVDQ_INT8;
+  p.eps = d->eps;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->in == SVDQ_BF16) return launch_rms<DT_BF16>(p, M, dev.sms, st);
+  if (d->in == SVDQ_FP16) return launch_rms<DT_FP16>(p, M, dev.sms, st);
+  return launch_rms<DT_FP32>(p, M, dev.sms, st);
+}
+
+svdq_status svdq_rope_load(const svdq_rope_desc* d, svdq_rope_t* out) {
+  if (!d || !out) return SVDQ_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (d->head_dim < 2 || d->head_dim > ROPE_MAX_D) return SVDQ_ERR_SHAPE;
+  if (d->axes < 1 || d->axes > SVDQ_ROPE_MAX_AXES) return SVDQ_ERR_SHAPE;
+  int64_t R = 0;
+  for (int a = 0; a < d->axes; ++a) {
+    if (d->axis_dim[a] < 2 || d->axis_dim[a] % 2 != 0 || d->axis_dim[a] > ROPE_MAX_D) return SVDQ_ERR_SHAPE;
+    R += d->axis_dim[a];
+  }
+  if (R > d->head_dim) return SVDQ_ERR_SHAPE;
+  if ((d->interleaved != 0 && d->interleaved != 1) || (d->shared != 0 && d->shared != 1)) return SVDQ_ERR_INVALID_ARG;
+  for (int a = 0; a < (d->shared ? 1 : d->axes); ++a)
+    if (!(d->theta[a] >= 1.0) || !(d->theta[a] <= 1e30)) return SVDQ_ERR_INVALID_ARG;
+  svdq_rope* h = new (std::nothrow) svdq_rope();
+  if (!h) return SVDQ_ERR_OOM;
+  h->axes = d->axes;
+  h->plan.D = static_cast<int>(d->head_dim);
+  h->plan.pairs = static_cast<int>(R / 2);
+  h->plan.interleaved = d->interleaved;
+  int pr = 0;
+  for (int a = 0; a < d->axes; ++a)
+    for (int i = 0; i < d->axis_dim[a] / 2; ++i, ++pr) {
+      const double e = d->shared ? 2.0 * pr / static_cast<double>(R) : 2.0 * i / static_cast<double>(d->axis_dim[a]);
+      h->plan.f[pr] = std::pow(d->theta[d->shared ? 0 : a], -e) / 3.14159265358979323846;
+      h->plan.axis[pr] = static_cast<uint8_t>(a);
+    }
+  *out = h;
+  return SVDQ_OK;
+}
+
+svdq_status svdq_rope_free(svdq_rope_t h) {
+  delete h;
+  return SVDQ_OK;
+}
+
+svdq_status svdq_rope_apply(svdq_rope_t h, svdq_dtype dtype, int64_t B, int64_t S, const svdq_rope_positions* pos,
+                            const svdq_rope_tensor* q, const svdq_rope_tensor* k, int inverse, void* stream) {
+  if (!h || !q) return SVDQ_ERR_INVALID_ARG;
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16 && dtype != SVDQ_FP32) return SVDQ_ERR_INVALID_ARG;
+  if (inverse != 0 && inverse != 1) return SVDQ_ERR_INVALID_ARG;
+  if (B < 0 || S < 0 || B > kRopeMaxTokens || S > kRopeMaxTokens || (B > 0 && S > kRopeMaxTokens / B)) return SVDQ_ERR_SHAPE;
+  const int es = dtype_size(dtype);
+  RopeParams p{};
+  const svdq_rope_tensor* in[2] = {q, k};
+  Nest from[2] = {}, to[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    const svdq_rope_tensor& t = *in[i];
+    if (t.heads < 0 || t.heads > 65536) return SVDQ_ERR_SHAPE;
+    for (int a = 0; a < 3; ++a) {
+      const int64_t n = a == 0 ? B : a == 1 ? S : t.heads;
+      if (t.stride[a] < 0 || t.out_stride[a] < 0) return SVDQ_ERR_SHAPE;
+      if (n > 1 && (t.stride[a] > kRopeMaxSpan / n || t.out_stride[a] > kRopeMaxSpan / n)) return SVDQ_ERR_SHAPE;
+    }
+    if (t.heads == 0 || B == 0 || S == 0) continue;
+    if (!t.x || !t.out) return SVDQ_ERR_INVALID_ARG;
+    if (!aligned(t.x, es) || !aligned(t.out, es)) return SVDQ_ERR_ALIGNMENT;
+    if (t.x == t.out)
+      for (int a = 0; a < 3; ++a)
+        if ((a == 0 ? B : a == 1 ? S : t.heads) > 1 && t.stride[a] != t.out_stride[a]) return SVDQ_ERR_INVALID_ARG;
+    from[i] = nest(t.x, B, S, t.heads, t.stride, h->plan.D, es);
+    to[i] = nest(t.out, B, S, t.heads, t.out_stride, h->plan.D, es);
+    if (!nests(to[i])) return SVDQ_ERR_SHAPE;
+    if (t.x != t.out && may_meet(from[i], to[i])) return SVDQ_ERR_INVALID_ARG;
+    p.t[i] = RopeTensor{t.x, t.out, static_cast<int>(t.heads), t.stride[0], t.stride[1], t.stride[2],
+                        t.out_stride[0], t.out_stride[1], t.out_stride[2]};
+    if (t.x != t.out && h->plan.D > 2 * h->plan.pairs) p.pass = 1;
+  }
+  if (may_meet(to[0], to[1]) || may_meet(to[0], from[1]) || may_meet(from[0], to[1])) return SVDQ_ERR_INVALID_ARG;
+  if (B == 0 || S == 0 || p.t[0].heads + p.t[1].heads == 0) return SVDQ_OK;
+  if (svdq_status s = rope_pos(pos, &p.pos); s != SVDQ_OK) return s;
+  DeviceInfo dev;
+  if (svdq_status s = device_info(&dev); s != SVDQ_OK) return s;
+  p.plan = h->plan;
+  p.S = S;
+  p.tokens = B * S;
+  p.sign = inverse ? -1.f : 1.f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SVDQ_BF16) return launch_rope<DT_BF16>(p, st);
+  if (dtype == SVDQ_FP16) return launch_rope<DT_FP16>(p, st);
+  return launch_rope<DT_FP32>(p, st);
+}
+
+svdq_status svdq_rope_table(svdq_rope_t h, int64_t B, int64_t S, const svdq_rope_positions* pos, float* table,
+                            void* stream) {
+  if (!h) return SVDQ_ERR_INVALID_ARG;
+  if (B < 0 || S < 0 || B > kRopeMaxTokens || S > kRopeMaxTokens || (B > 0 && S > kRopeMaxTokens / B)) return SVDQ_ERR_SHAPE;
+  if (B == 0 || S == 0) return SVDQ_OK;
+  if (!table) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned(table, 8)) return SVDQ_ERR_ALIGNMENT;
+  RopeTableParams p{};
+  if (svdq_status s = rope_pos(pos, &p.pos); s != SVDQ_OK) return s;
+  DeviceInfo dev;
+  if (svdq_status s = device_info(&dev); s != SVDQ_OK) return s;
+  p.plan = h->plan;
+  p.S = S;
+  p.tokens = B * S;
+  p.table = reinterpret_cast<float2*>(table);
+  const int64_t blocks = cdiv(p.tokens * p.plan.pairs, ROPE_THREADS);
+  if (blocks > INT32_MAX) return SVDQ_ERR_SHAPE;
+  LaunchCfg lc(dim3(static_cast<unsigned>(blocks)), dim3(ROPE_THREADS), 0, static_cast<cudaStream_t>(stream));
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rope_table_kernel, p));
+  return SVDQ_OK;
+}
+
+}  // extern "C"

@@ -38,6 +38,8 @@ EXPORTED = [
     "svdq_w4a4_gemm_lowrank_up_qkv", "svdq_linear_forward_qkv",
     "svdq_w4a4_gemm_lowrank_up_chain", "svdq_linear_forward_chain", "svdq_device_error_site",
     "svdq_set_deterministic",
+    "svdq_dense_forward", "svdq_rms_quantize8",
+    "svdq_rope_load", "svdq_rope_free", "svdq_rope_apply", "svdq_rope_table",
 ]
 
 
@@ -108,6 +110,12 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.svdq_prep_residual_quantize.argtypes = [st, vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, vp, vp,
                                               ctypes.POINTER(ctypes.c_int32), vp]
     L.svdq_quantize_act_lowrank_down_static.argtypes = [st, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    L.svdq_dense_forward.argtypes = [vp, vp]
+    L.svdq_rms_quantize8.argtypes = [vp, vp]
+    L.svdq_rope_load.argtypes = [vp, ctypes.POINTER(vp)]
+    L.svdq_rope_free.argtypes = [vp]
+    L.svdq_rope_apply.argtypes = [vp, st, i64, i64, vp, vp, vp, st, vp]
+    L.svdq_rope_table.argtypes = [vp, i64, i64, vp, vp, vp]
     L.svdq_status_string.argtypes = [st]
     L.svdq_status_string.restype = ctypes.c_char_p
     L.svdq_version.restype = ctypes.c_char_p
@@ -352,3 +360,299 @@ def untile_nvfp4_scales(buf: np.ndarray, M: int, K: int) -> np.ndarray:
     b = np.arange(K // 16)[None, :]
     off = ((m // 128) * (K // 64) + b // 4) * 512 + (m % 32) * 16 + ((m // 32) % 4) * 4 + b % 4
     return buf[off]
+
+
+# ------------------------------------- operators around the 4-bit layers
+# These take torch tensors whose shapes and strides say what the C structs
+# spell out (2-D tensors with contiguous rows, any row distance).  They run on
+# the tensors' own device, on `stream` or that device's current stream.
+BF16, FP16, FP32, E4M3, INT8 = range(5)
+ACTS = {None: 0, "none": 0, "gelu": 1, "silu": 2}
+_DTYPES: dict = {}
+
+
+class DenseDesc(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_int), ("out", ctypes.c_int), ("act", ctypes.c_int),
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+        ("a_scale", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("device_error", ctypes.c_void_p),
+    ]
+
+
+class Rms8Desc(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_int), ("out", ctypes.c_int), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("weight_rows", ctypes.c_int64),
+        ("norm", ctypes.c_int), ("eps", ctypes.c_float),
+        ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("scales", ctypes.c_void_p),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int64), ("axes", ctypes.c_int), ("axis_dim", ctypes.c_int64 * 4),
+        ("theta", ctypes.c_double * 4), ("interleaved", ctypes.c_int), ("shared", ctypes.c_int),
+    ]
+
+
+class RopePositions(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("type", ctypes.c_int), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("axis_stride", ctypes.c_int64)]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
+def _dtype(t, allowed, what: str) -> int:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
+                        torch.float8_e4m3fn: E4M3, torch.int8: INT8})
+    d = _DTYPES.get(t.dtype)
+    if d not in allowed:
+        raise TypeError(f"{what}: dtype {t.dtype} is not supported here")
+    return d
+
+
+def _matrix(t, rows, cols, like, what: str) -> int:
+    """Row distance of a [rows x cols] tensor with contiguous rows on `like`'s device."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.device != like.device:
+        raise ValueError(f"{what} is on {t.device}, expected {like.device}")
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return ld
+
+
+def _vector(t, n, dtype, like, what: str) -> None:
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(n,)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{what} is on {t.device}, expected {like.device}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _same_dtype(t, like, what: str) -> None:
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {like.dtype}")
+
+
+def _rows_of(t, rows_each, M, cols, like, what: str):
+    """(row distance, rows each) of a [G x cols] tensor (or [cols]: one row)
+    whose row g serves rows g * rows_each .. of M."""
+    if t.dim() == 1:
+        _vector(t, cols, like.dtype, like, what)
+        return cols, max(M, 1)
+    _same_dtype(t, like, what)
+    rows_each = int(rows_each) or max(M, 1)
+    if rows_each < 1:
+        raise ValueError(f"{what}: rows each must be positive")
+    return _matrix(t, -(-M // rows_each), cols, like, what), rows_each
+
+
+def _run_on(t, stream, call, *args) -> int:
+    """call(*args, stream) with t's device current."""
+    import torch
+    if t.device.type != "cuda":
+        if torch.cuda.is_available():
+            raise ValueError(f"the tensors are on {t.device}, expected a CUDA device")
+        return call(*args, 0 if stream is None else int(stream))   # the library reports the missing device
+    dev = t.device.index
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return call(*args, _stream(stream))
+    return call(*args, _stream(stream))
+
+
+def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate=None, gate_rows=0,
+                  residual=None, device_error=None, stream=None):
+    """y = residual + gate * act(a_scale w_scale (a @ w.T) + bias), written to
+    and returned as ``y`` (svdq_dense_forward).
+
+    a [M, K] and w [N, K] are bf16, fp16, float8_e4m3fn or int8; y [M, N],
+    bias [N], gate and residual [M, N] are bf16 or fp16 (the operands' type
+    where that is one of them).  a_scale [M] and w_scale [N] are fp32 and for
+    8-bit operands only.  act: None, "gelu" (tanh form) or "silu".  gate is [N]
+    or [ceil(M / gate_rows), N].  residual may be y."""
+    kind = _dtype(a, (BF16, FP16, E4M3, INT8), "a")
+    out = _dtype(y, (BF16, FP16), "y")
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a and w must be matrices")
+    M, K = a.shape
+    N = w.shape[0]
+    _same_dtype(w, a, "w")
+    if act not in ACTS:
+        raise ValueError(f"act: {act!r}, expected one of {list(ACTS)}")
+    ldg = ldr = 0
+    lda, ldw, ldy = _matrix(a, M, K, a, "a"), _matrix(w, N, K, a, "w"), _matrix(y, M, N, a, "y")
+    if a_scale is not None or w_scale is not None:
+        import torch
+        if a_scale is not None:
+            _vector(a_scale, M, torch.float32, a, "a_scale")
+        if w_scale is not None:
+            _vector(w_scale, N, torch.float32, a, "w_scale")
+    if bias is not None:
+        _vector(bias, N, y.dtype, y, "bias")
+    if gate is not None:
+        ldg, gate_rows = _rows_of(gate, gate_rows, M, N, y, "gate")
+    if residual is not None:
+        _same_dtype(residual, y, "residual")
+        ldr = _matrix(residual, M, N, y, "residual")
+    if device_error is not None:
+        import torch
+        _vector(device_error, 1, torch.int32, a, "device_error")
+    d = DenseDesc(kind, out, ACTS[act], M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, _ptr(a_scale), _ptr(w_scale),
+                  _ptr(bias), _ptr(gate), ldg, int(gate_rows), _ptr(residual), ldr, y.data_ptr(), ldy,
+                  _ptr(device_error))
+    _check(_run_on(a, stream, lib().svdq_dense_forward, ctypes.byref(d)), "svdq_dense_forward")
+    return y
+
+
+def rms_quantize8(x, codes, scales, residual=None, h=None, weight=None, weight_rows=0, eps=1e-6, norm=True,
+                  stream=None):
+    """h = x + residual; codes, scales = the RMS norm of h times weight in 8
+    bits (svdq_rms_quantize8), or of h times weight itself with ``norm=False``.
+
+    x, residual and h [M, K] are bf16, fp16 or fp32, codes [M, K] is
+    float8_e4m3fn or int8, scales [M] fp32.  weight is [K] or
+    [ceil(M / weight_rows), K].  residual, h and weight may be None; h may be x
+    or residual.  Returns (codes, scales)."""
+    kind = _dtype(x, (BF16, FP16, FP32), "x")
+    out = _dtype(codes, (E4M3, INT8), "codes")
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    M, K = x.shape
+    import torch
+    ldr = ldh = ldw = 0
+    ldx, ldc = _matrix(x, M, K, x, "x"), _matrix(codes, M, K, x, "codes")
+    _vector(scales, M, torch.float32, x, "scales")
+    if residual is not None:
+        _same_dtype(residual, x, "residual")
+        ldr = _matrix(residual, M, K, x, "residual")
+    if h is not None:
+        _same_dtype(h, x, "h")
+        ldh = _matrix(h, M, K, x, "h")
+    if weight is not None:
+        ldw, weight_rows = _rows_of(weight, weight_rows, M, K, x, "weight")
+    d = Rms8Desc(kind, out, M, K, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(h), ldh, _ptr(weight), ldw,
+                 int(weight_rows), 1 if norm else 0, float(eps), codes.data_ptr(), ldc, scales.data_ptr())
+    _check(_run_on(x, stream, lib().svdq_rms_quantize8, ctypes.byref(d)), "svdq_rms_quantize8")
+    return codes, scales
+
+
+class RopeAxes:
+    """Rotary positions with several axes: owns a library handle
+    (``svdq_rope_t``; host memory only, usable on every device)."""
+
+    def __init__(self, head_dim, axis_dims, theta=10000.0, interleaved=True, shared=False):
+        """``axis_dims``: rotated elements per axis (even, at most four axes,
+        together at most head_dim).  ``theta``: one base, or one per axis.
+        ``interleaved``: pairs (2p, 2p + 1), else (p, p + R/2).  ``shared``: the
+        axes are sections of one line of frequencies."""
+        dims = [int(v) for v in axis_dims]
+        thetas = [float(v) for v in theta] if isinstance(theta, (list, tuple)) else [float(theta)] * max(1, len(dims))
+        self.head_dim, self.axis_dims, self.handle = int(head_dim), dims, None
+        if len(dims) > 4 or len(thetas) != max(1, len(dims)):
+            raise SvdqError(2, "svdq_rope_load")
+        d = RopeDesc(self.head_dim, len(dims), (ctypes.c_int64 * 4)(*dims), (ctypes.c_double * 4)(*thetas),
+                     1 if interleaved else 0, 1 if shared else 0)
+        h = ctypes.c_void_p(0)
+        self._lib = lib()
+        _check(self._lib.svdq_rope_load(ctypes.byref(d), ctypes.byref(h)), "svdq_rope_load")
+        self.handle = h
+
+    def _positions(self, pos, B, S, like):
+        """pos [S, axes] (shared by the sequences), [B, S, axes] or [B * S, axes]."""
+        import torch
+        types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+        if pos.dtype not in types:
+            raise TypeError(f"pos: dtype {pos.dtype} is not supported here")
+        if like is not None and pos.device != like.device:
+            raise ValueError(f"pos is on {pos.device}, expected {like.device}")
+        n, shape, st = len(self.axis_dims), tuple(pos.shape), pos.stride()
+        if shape == (B * S, n):
+            return RopePositions(pos.data_ptr(), types[pos.dtype], S * st[0], st[0], st[1])
+        if shape == (S, n):
+            return RopePositions(pos.data_ptr(), types[pos.dtype], 0, st[0], st[1])
+        if shape == (B, S, n):
+            return RopePositions(pos.data_ptr(), types[pos.dtype], *st)
+        raise ValueError(f"pos: shape {shape}, expected {(S, n)}, {(B * S, n)} or {(B, S, n)}")
+
+    def _tensor(self, x, out, B, S, like, what):
+        if x.dim() not in (3, 4) or x.shape[-1] != self.head_dim:
+            raise ValueError(f"{what}: shape {tuple(x.shape)}, expected [(B,) S, H, {self.head_dim}]")
+        if x.device != like.device:
+            raise ValueError(f"{what} is on {x.device}, expected {like.device}")
+        _same_dtype(x, like, what)
+        if (x.shape[0] if x.dim() == 4 else 1) != B or x.shape[-3] != S:
+            raise ValueError(f"{what}: shape {tuple(x.shape)} does not fit {B} sequences of {S} tokens")
+        if out is None:
+            out = x
+        elif out.shape != x.shape or out.device != x.device:
+            raise ValueError(f"{what}_out: shape {tuple(out.shape)} on {out.device}, expected {tuple(x.shape)} on {x.device}")
+        _same_dtype(out, x, what + "_out")
+        if x.stride(-1) != 1 or out.stride(-1) != 1:
+            raise ValueError(f"{what}: the elements of a head must be contiguous")
+        b = (lambda t: t.stride(0)) if x.dim() == 4 else (lambda t: 0)
+        return RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[-2], (b(x), x.stride(-3), x.stride(-2)),
+                          (b(out), out.stride(-3), out.stride(-2))), out
+
+    def apply(self, q, pos, k=None, q_out=None, k_out=None, inverse=False, stream=None):
+        """Rotate q and k ([S, H, D] or [B, S, H, D], any strides between heads,
+        tokens and sequences; bf16, fp16 or fp32) into q_out and k_out (None: in
+        place); ``inverse`` turns back, which is the gradient.  pos is int32,
+        int64 or fp32.  Returns q's output, or both."""
+        kind = _dtype(q, (BF16, FP16, FP32), "q")
+        if q.dim() not in (3, 4):
+            raise ValueError(f"q: shape {tuple(q.shape)}, expected [(B,) S, H, {self.head_dim}]")
+        B, S = (q.shape[0] if q.dim() == 4 else 1), q.shape[-3]
+        tq, q_out = self._tensor(q, q_out, B, S, q, "q")
+        tk = None
+        if k is not None:
+            tk, k_out = self._tensor(k, k_out, B, S, q, "k")
+        p = self._positions(pos, B, S, q)
+        _check(_run_on(q, stream, self._lib.svdq_rope_apply, self.handle, kind, B, S, ctypes.byref(p), ctypes.byref(tq),
+                       None if tk is None else ctypes.byref(tk), 1 if inverse else 0), "svdq_rope_apply")
+        return q_out if k is None else (q_out, k_out)
+
+    def table(self, pos, table, stream=None):
+        """(cos, sin) of every token and pair into ``table`` (contiguous fp32 of
+        tokens x R elements), the ``rope`` argument of ``linear_forward_qkv``
+        when R = 128.  pos is [tokens, axes]."""
+        import torch
+        if pos.dim() != 2:
+            raise ValueError(f"pos: shape {tuple(pos.shape)}, expected [tokens, {len(self.axis_dims)}]")
+        S = pos.shape[0]
+        if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() != S * sum(self.axis_dims):
+            raise ValueError(f"table: expected {S * sum(self.axis_dims)} contiguous fp32 elements")
+        p = self._positions(pos, 1, S, table)
+        _check(_run_on(pos, stream, self._lib.svdq_rope_table, self.handle, 1, S, ctypes.byref(p), table.data_ptr()),
+               "svdq_rope_table")
+        return table
+
+    def close(self) -> None:
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            self._lib.svdq_rope_free(self.handle)
+            self.handle = ctypes.c_void_p(0)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -486,6 +486,184 @@ svdq_status svdq_debug_set_fault(svdq_weights_t h, uint32_t mask, uint32_t timeo
  */
 svdq_status svdq_selftest_division(int variant, unsigned long long* mismatches);
 
+/* ------------------------------------------------------------------------
+ * Operators around the 4-bit layers of a transformer block: layers kept at 16
+ * or 8 bits, the norm in front of an 8-bit layer, and rotary positions.  No
+ * counterpart on the pages (their runtime leaves these to the host
+ * framework); they let a block whose linears are this library's run without
+ * one.  The calls take every buffer from the caller, allocate nothing, keep
+ * nothing between calls (calls may overlap freely, on any streams, in
+ * captured graphs too) and run on the current device, whose memory the
+ * buffers must be.  Outputs must not overlap inputs except where a call says
+ * so; overlaps that the host can see return SVDQ_ERR_INVALID_ARG.  Row
+ * distances (ld*) are in elements; that of a single row is not looked at.  A
+ * call for no rows (M = 0, B or S = 0) returns SVDQ_OK and does nothing.
+ */
+typedef enum {
+  SVDQ_BF16 = 0,
+  SVDQ_FP16 = 1,
+  SVDQ_FP32 = 2,
+  SVDQ_E4M3 = 3,
+  SVDQ_INT8 = 4
+} svdq_dtype;
+
+typedef enum {
+  SVDQ_ACT_NONE = 0,
+  SVDQ_ACT_GELU = 1,   /* tanh form, as SVDQ_EPI_GELU */
+  SVDQ_ACT_SILU = 2    /* v / (1 + exp(-v)) */
+} svdq_act;
+
+/*
+ * Dense linear layer with a fused epilogue:
+ *   y[m,n] = residual[m,n] + gate[m / gate_rows, n] *
+ *            act( a_scale[m] w_scale[n] sum_k a[m,k] w[n,k] + bias[n] )
+ * with every term after the product optional (NULL, SVDQ_ACT_NONE).  The sum
+ * is kept in fp32 (int32, exact, for INT8), the epilogue in fp32, and y is
+ * rounded once.  The result does not depend on timing: equal calls give equal
+ * bits.
+ *   in   operand type: SVDQ_BF16, SVDQ_FP16, SVDQ_E4M3 or SVDQ_INT8
+ *   out  type of y, bias, gate and residual: SVDQ_BF16 or SVDQ_FP16, and
+ *        equal to `in` where that is one of them
+ *   a    [M x K], w [N x K] (the layout of torch.nn.Linear.weight): 16-byte
+ *        aligned, rows a multiple of 16 bytes apart (else
+ *        SVDQ_ERR_ALIGNMENT); K itself is free, and what lies between K and
+ *        the row distance is not read
+ *   a_scale fp32 [M], w_scale fp32 [N]: 8-bit operands only
+ *   gate [ceil(M / gate_rows) x N]: one row per image, say, or one row per
+ *        token (gate_rows = 1)
+ *   residual [M x N]; ldr = 0 adds one row to every token; may be y itself
+ *        (same pointer and row distance)
+ *   device_error device int, set to a nonzero wait-site code if a bounded
+ *        wait expires (never cleared by the library); may be NULL, such a
+ *        failure then is reported to no one
+ * 0 <= M <= 2^24, 1 <= N <= 2^24, 1 <= K <= 65536, and at most 2^27 tiles of
+ * 16 tokens by 128 features.  Rows beyond M are left as they were.
+ */
+typedef struct {
+  svdq_dtype in, out;
+  svdq_act act;
+  int64_t M, N, K;
+  const void* a;
+  int64_t lda;
+  const void* w;
+  int64_t ldw;
+  const float* a_scale;
+  const float* w_scale;
+  const void* bias;
+  const void* gate;
+  int64_t ldg, gate_rows;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  int* device_error;
+} svdq_dense_desc;
+svdq_status svdq_dense_forward(const svdq_dense_desc* desc, void* stream);
+
+/*
+ * RMS norm with the residual's addition, quantised to 8 bits with one scale
+ * per row: the activations of an 8-bit svdq_dense_forward.
+ *   h = x + residual                                (rounded to `in`)
+ *   v = h rsqrt(mean_k(h^2) + eps) weight           (norm = 1; weight optional)
+ *   v = h weight                                    (norm = 0: quantise only,
+ *                                                    also for weights, row by row)
+ *   scales[m] = max_k |v| / top,  codes[m,k] = v / scales[m],
+ * rounded to nearest even; top = 448 (E4M3) or 127 (INT8).  The codes are
+ * computed as t (top / max|t|) with t = h weight in fp32, in which the norm
+ * cancels: they do not depend on the order of any sum.
+ * A row whose largest |h weight| is below 2^-118 gets zero codes and the
+ * scale 0.  A row that holds a NaN or an infinity, or whose product with the
+ * weight overflows fp32, gets the scale NaN; its codes say nothing.
+ *   in   SVDQ_BF16, SVDQ_FP16 or SVDQ_FP32: type of x, residual, h, weight
+ *   out  SVDQ_E4M3 or SVDQ_INT8
+ *   residual [M x K] or NULL; h [M x K] (written) or NULL; h may be x or
+ *        residual itself (same pointer and row distance)
+ *   weight [ceil(M / weight_rows) x K] or NULL: row m uses weight row
+ *        m / weight_rows
+ * 0 <= M < 2^31, 1 <= K <= 32768, any alignment and row distance (ldx, ldr
+ * and ldw may be 0: one row for all; at most 2^28); 16-byte aligned rows run
+ * fastest.
+ */
+typedef struct {
+  svdq_dtype in, out;
+  int64_t M, K;
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  void* h;
+  int64_t ldh;
+  const void* weight;
+  int64_t ldw, weight_rows;
+  int norm;
+  float eps;               /* 0 < eps < 1 (norm = 1) */
+  void* codes;
+  int64_t ldc;
+  float* scales;
+} svdq_rms8_desc;
+svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream);
+
+/*
+ * Rotary positions with several axes (text index, time, height, width, ...).
+ * A head's first R = sum axis_dim elements rotate in R/2 pairs: the first
+ * axis_dim[0] / 2 pairs by the token's position on axis 0, the next by axis
+ * 1, and so on.  Pair i of axis a, pair p of all, turns by
+ *   pos[token, a] * theta[a]^(-2 i / axis_dim[a])     (shared = 0)
+ *   pos[token, a] * theta[0]^(-2 p / R)               (shared = 1: the axes
+ *                                                      are sections of one line)
+ * radians: (u, v) <- (u cos - v sin, u sin + v cos).  Its elements are
+ * (2p, 2p + 1) with interleaved = 1, (p, p + R/2) with interleaved = 0.
+ * Elements R .. head_dim - 1 pass through.  Angles are formed and reduced in
+ * fp64, cos and sin and the rotation are fp32, rounded once.
+ *   2 <= head_dim <= 256; 1 <= axes <= 4; axis_dim even; 1 <= theta <= 1e30.
+ * The handle is host memory only: it serves every device and any number of
+ * calls at once.
+ */
+#define SVDQ_ROPE_MAX_AXES 4
+typedef struct svdq_rope* svdq_rope_t;
+typedef struct {
+  int64_t head_dim;
+  int axes;
+  int64_t axis_dim[SVDQ_ROPE_MAX_AXES];
+  double theta[SVDQ_ROPE_MAX_AXES];
+  int interleaved, shared;
+} svdq_rope_desc;
+svdq_status svdq_rope_load(const svdq_rope_desc* desc, svdq_rope_t* out);
+svdq_status svdq_rope_free(svdq_rope_t h);   /* NULL is a no-op */
+
+/* Positions: element (batch b, token s, axis a) at p[b * batch_stride +
+ * s * token_stride + a * axis_stride]; batch_stride = 0 shares them. */
+typedef enum { SVDQ_POS_INT32 = 0, SVDQ_POS_INT64 = 1, SVDQ_POS_FP32 = 2 } svdq_pos_type;
+typedef struct {
+  const void* p;
+  svdq_pos_type type;
+  int64_t batch_stride, token_stride, axis_stride;
+} svdq_rope_positions;
+
+/* Heads of head_dim contiguous elements; strides (batch, token, head) in
+ * elements, in any order ([B, S, H, D] and [B, H, S, D] alike).  Output heads
+ * must not meet; out may be x itself with the same strides. */
+typedef struct {
+  const void* x;
+  void* out;
+  int64_t heads;
+  int64_t stride[3], out_stride[3];
+} svdq_rope_tensor;
+
+/* Rotate q and k (k may be NULL, and either may have 0 heads) of B sequences
+ * of S tokens, of type SVDQ_BF16, SVDQ_FP16 or SVDQ_FP32; inverse = 1 turns
+ * the other way, which undoes the rotation and takes a gradient of the output
+ * to the gradient of the input.  B * S <= 2^31. */
+svdq_status svdq_rope_apply(svdq_rope_t h, svdq_dtype dtype, int64_t B, int64_t S,
+                            const svdq_rope_positions* pos, const svdq_rope_tensor* q,
+                            const svdq_rope_tensor* k, int inverse, void* stream);
+
+/* (cos, sin) of every token and pair, fp32 [B * S x R/2 x 2] (8-byte
+ * aligned): with head_dim = 128, R = 128 and interleaved pairs the `rope`
+ * argument of svdq_linear_forward_qkv. */
+svdq_status svdq_rope_table(svdq_rope_t h, int64_t B, int64_t S, const svdq_rope_positions* pos,
+                            float* table, void* stream);
+
 /* Human-readable name of a status code (static storage); no counterpart on
  * the pages. */
 const char* svdq_status_string(svdq_status s);
