@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -369,6 +370,7 @@ def untile_nvfp4_scales(buf: np.ndarray, M: int, K: int) -> np.ndarray:
 BF16, FP16, FP32, E4M3, INT8 = range(5)
 ACTS = {None: 0, "none": 0, "gelu": 1, "silu": 2}
 _DTYPES: dict = {}
+_POS_TYPES: dict = {}
 
 
 class DenseDesc(ctypes.Structure):
@@ -414,70 +416,80 @@ class RopeTensor(ctypes.Structure):
                 ("stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
 
-def _dtype(t, allowed, what: str) -> int:
+# The structs again as struct formats: packing one takes a quarter of the time
+# of filling a ctypes.Structure, which a call on a few tokens would feel.
+_DENSE = struct.Struct("@3i4x3q" "Pq" "Pq" "3P" "P2q" "Pq" "Pq" "P")
+_RMS8 = struct.Struct("@2i2q" "Pq" "Pq" "Pq" "P2q" "if" "Pq" "P")
+_ROPE_POS = struct.Struct("@Pi4x3q")
+_ROPE_TENSOR = struct.Struct("@2P7q")
+
+
+def _dtypes() -> dict:
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
                         torch.float8_e4m3fn: E4M3, torch.int8: INT8})
-    d = _DTYPES.get(t.dtype)
+    return _DTYPES
+
+
+def _dtype(t, allowed, what: str) -> int:
+    d = _dtypes().get(t.dtype)
     if d not in allowed:
         raise TypeError(f"{what}: dtype {t.dtype} is not supported here")
     return d
 
 
-def _matrix(t, rows, cols, like, what: str) -> int:
-    """Row distance of a [rows x cols] tensor with contiguous rows on `like`'s device."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if t.device != like.device:
-        raise ValueError(f"{what} is on {t.device}, expected {like.device}")
+def _differs(t, shape, dtype, dev, what: str):
+    """Raise for the first of t's shape, dtype and device that is not as given."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    raise ValueError(f"{what} is on {t.device}, expected the other tensors' device")
+
+
+def _matrix(t, rows, cols, dtype, dev, what: str) -> int:
+    """Row distance of a [rows x cols] tensor with contiguous rows."""
+    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev:
+        _differs(t, (rows, cols), dtype, dev, what)
     ld, step = t.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
     return ld
 
 
-def _vector(t, n, dtype, like, what: str) -> None:
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(n,)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{what} is on {t.device}, expected {like.device}")
-    if n > 1 and t.stride(0) != 1:
+def _vector(t, n, dtype, dev, what: str) -> int:
+    """Address of a contiguous [n] tensor."""
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != dev:
+        _differs(t, (n,), dtype, dev, what)
+    if n > 1 and t.stride() != (1,):
         raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
-def _same_dtype(t, like, what: str) -> None:
-    if t.dtype != like.dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected {like.dtype}")
-
-
-def _rows_of(t, rows_each, M, cols, like, what: str):
+def _rows_of(t, rows_each, M, cols, dtype, dev, what: str):
     """(row distance, rows each) of a [G x cols] tensor (or [cols]: one row)
     whose row g serves rows g * rows_each .. of M."""
     if t.dim() == 1:
-        _vector(t, cols, like.dtype, like, what)
+        _vector(t, cols, dtype, dev, what)
         return cols, max(M, 1)
-    _same_dtype(t, like, what)
     rows_each = int(rows_each) or max(M, 1)
     if rows_each < 1:
         raise ValueError(f"{what}: rows each must be positive")
-    return _matrix(t, -(-M // rows_each), cols, like, what), rows_each
+    return _matrix(t, -(-M // rows_each), cols, dtype, dev, what), rows_each
 
 
-def _run_on(t, stream, call, *args) -> int:
-    """call(*args, stream) with t's device current."""
+def _run_on(dev: int, stream, call, *args) -> int:
+    """call(*args, stream) with CUDA device `dev` current."""
     import torch
-    if t.device.type != "cuda":
+    if dev < 0:
         if torch.cuda.is_available():
-            raise ValueError(f"the tensors are on {t.device}, expected a CUDA device")
+            raise ValueError("the tensors are on the CPU, expected a CUDA device")
         return call(*args, 0 if stream is None else int(stream))   # the library reports the missing device
-    dev = t.device.index
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return call(*args, _stream(stream))
-    return call(*args, _stream(stream))
+            return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream))
+    return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream))
 
 
 def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate=None, gate_rows=0,
@@ -490,37 +502,38 @@ def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate
     where that is one of them).  a_scale [M] and w_scale [N] are fp32 and for
     8-bit operands only.  act: None, "gelu" (tanh form) or "silu".  gate is [N]
     or [ceil(M / gate_rows), N].  residual may be y."""
-    kind = _dtype(a, (BF16, FP16, E4M3, INT8), "a")
-    out = _dtype(y, (BF16, FP16), "y")
+    kind, out = _dtype(a, (BF16, FP16, E4M3, INT8), "a"), _dtype(y, (BF16, FP16), "y")
     if a.dim() != 2 or w.dim() != 2:
         raise ValueError("a and w must be matrices")
-    M, K = a.shape
-    N = w.shape[0]
-    _same_dtype(w, a, "w")
     if act not in ACTS:
         raise ValueError(f"act: {act!r}, expected one of {list(ACTS)}")
-    ldg = ldr = 0
-    lda, ldw, ldy = _matrix(a, M, K, a, "a"), _matrix(w, N, K, a, "w"), _matrix(y, M, N, a, "y")
-    if a_scale is not None or w_scale is not None:
+    M, K = a.shape
+    N = w.shape[0]
+    dev, it, ot = a.get_device(), a.dtype, y.dtype
+    lda, ldw = _matrix(a, M, K, it, dev, "a"), _matrix(w, N, K, it, dev, "w")
+    ldy = _matrix(y, M, N, ot, dev, "y")
+    sa = sw = pb = pg = pr = pe = ldg = ldr = 0
+    if a_scale is not None or w_scale is not None or device_error is not None:
         import torch
         if a_scale is not None:
-            _vector(a_scale, M, torch.float32, a, "a_scale")
+            sa = _vector(a_scale, M, torch.float32, dev, "a_scale")
         if w_scale is not None:
-            _vector(w_scale, N, torch.float32, a, "w_scale")
+            sw = _vector(w_scale, N, torch.float32, dev, "w_scale")
+        if device_error is not None:
+            pe = _vector(device_error, 1, torch.int32, dev, "device_error")
     if bias is not None:
-        _vector(bias, N, y.dtype, y, "bias")
+        pb = _vector(bias, N, ot, dev, "bias")
     if gate is not None:
-        ldg, gate_rows = _rows_of(gate, gate_rows, M, N, y, "gate")
+        ldg, gate_rows = _rows_of(gate, gate_rows, M, N, ot, dev, "gate")
+        pg = gate.data_ptr()
     if residual is not None:
-        _same_dtype(residual, y, "residual")
-        ldr = _matrix(residual, M, N, y, "residual")
-    if device_error is not None:
-        import torch
-        _vector(device_error, 1, torch.int32, a, "device_error")
-    d = DenseDesc(kind, out, ACTS[act], M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, _ptr(a_scale), _ptr(w_scale),
-                  _ptr(bias), _ptr(gate), ldg, int(gate_rows), _ptr(residual), ldr, y.data_ptr(), ldy,
-                  _ptr(device_error))
-    _check(_run_on(a, stream, lib().svdq_dense_forward, ctypes.byref(d)), "svdq_dense_forward")
+        ldr = _matrix(residual, M, N, ot, dev, "residual")
+        pr = residual.data_ptr()
+    d = _DENSE.pack(kind, out, ACTS[act], M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, sa, sw, pb, pg, ldg, gate_rows,
+                    pr, ldr, y.data_ptr(), ldy, pe)
+    code = _run_on(dev, stream, lib().svdq_dense_forward, d)
+    if code:
+        raise SvdqError(code, "svdq_dense_forward")
     return y
 
 
@@ -533,26 +546,29 @@ def rms_quantize8(x, codes, scales, residual=None, h=None, weight=None, weight_r
     float8_e4m3fn or int8, scales [M] fp32.  weight is [K] or
     [ceil(M / weight_rows), K].  residual, h and weight may be None; h may be x
     or residual.  Returns (codes, scales)."""
-    kind = _dtype(x, (BF16, FP16, FP32), "x")
-    out = _dtype(codes, (E4M3, INT8), "codes")
+    import torch
+    kind, out = _dtype(x, (BF16, FP16, FP32), "x"), _dtype(codes, (E4M3, INT8), "codes")
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     M, K = x.shape
-    import torch
-    ldr = ldh = ldw = 0
-    ldx, ldc = _matrix(x, M, K, x, "x"), _matrix(codes, M, K, x, "codes")
-    _vector(scales, M, torch.float32, x, "scales")
+    dev, it = x.get_device(), x.dtype
+    ldx, ldc = _matrix(x, M, K, it, dev, "x"), _matrix(codes, M, K, codes.dtype, dev, "codes")
+    ps = _vector(scales, M, torch.float32, dev, "scales")
+    pr = ph = pw = ldr = ldh = ldw = 0
     if residual is not None:
-        _same_dtype(residual, x, "residual")
-        ldr = _matrix(residual, M, K, x, "residual")
+        ldr = _matrix(residual, M, K, it, dev, "residual")
+        pr = residual.data_ptr()
     if h is not None:
-        _same_dtype(h, x, "h")
-        ldh = _matrix(h, M, K, x, "h")
+        ldh = _matrix(h, M, K, it, dev, "h")
+        ph = h.data_ptr()
     if weight is not None:
-        ldw, weight_rows = _rows_of(weight, weight_rows, M, K, x, "weight")
-    d = Rms8Desc(kind, out, M, K, x.data_ptr(), ldx, _ptr(residual), ldr, _ptr(h), ldh, _ptr(weight), ldw,
-                 int(weight_rows), 1 if norm else 0, float(eps), codes.data_ptr(), ldc, scales.data_ptr())
-    _check(_run_on(x, stream, lib().svdq_rms_quantize8, ctypes.byref(d)), "svdq_rms_quantize8")
+        ldw, weight_rows = _rows_of(weight, weight_rows, M, K, it, dev, "weight")
+        pw = weight.data_ptr()
+    d = _RMS8.pack(kind, out, M, K, x.data_ptr(), ldx, pr, ldr, ph, ldh, pw, ldw, weight_rows, 1 if norm else 0, eps,
+                   codes.data_ptr(), ldc, ps)
+    code = _run_on(dev, stream, lib().svdq_rms_quantize8, d)
+    if code:
+        raise SvdqError(code, "svdq_rms_quantize8")
     return codes, scales
 
 
@@ -577,58 +593,65 @@ class RopeAxes:
         _check(self._lib.svdq_rope_load(ctypes.byref(d), ctypes.byref(h)), "svdq_rope_load")
         self.handle = h
 
-    def _positions(self, pos, B, S, like):
+    def _positions(self, pos, B, S, dev):
         """pos [S, axes] (shared by the sequences), [B, S, axes] or [B * S, axes]."""
-        import torch
-        types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
-        if pos.dtype not in types:
+        if not _POS_TYPES:
+            import torch
+            _POS_TYPES.update({torch.int32: 0, torch.int64: 1, torch.float32: 2})
+        kind = _POS_TYPES.get(pos.dtype)
+        if kind is None:
             raise TypeError(f"pos: dtype {pos.dtype} is not supported here")
-        if like is not None and pos.device != like.device:
-            raise ValueError(f"pos is on {pos.device}, expected {like.device}")
-        n, shape, st = len(self.axis_dims), tuple(pos.shape), pos.stride()
+        if pos.get_device() != dev:
+            raise ValueError(f"pos is on {pos.device}, expected the other tensors' device")
+        n, shape, st = len(self.axis_dims), pos.shape, pos.stride()
         if shape == (B * S, n):
-            return RopePositions(pos.data_ptr(), types[pos.dtype], S * st[0], st[0], st[1])
+            return _ROPE_POS.pack(pos.data_ptr(), kind, S * st[0], st[0], st[1])
         if shape == (S, n):
-            return RopePositions(pos.data_ptr(), types[pos.dtype], 0, st[0], st[1])
+            return _ROPE_POS.pack(pos.data_ptr(), kind, 0, st[0], st[1])
         if shape == (B, S, n):
-            return RopePositions(pos.data_ptr(), types[pos.dtype], *st)
-        raise ValueError(f"pos: shape {shape}, expected {(S, n)}, {(B * S, n)} or {(B, S, n)}")
+            return _ROPE_POS.pack(pos.data_ptr(), kind, *st)
+        raise ValueError(f"pos: shape {tuple(shape)}, expected {(S, n)}, {(B * S, n)} or {(B, S, n)}")
 
-    def _tensor(self, x, out, B, S, like, what):
-        if x.dim() not in (3, 4) or x.shape[-1] != self.head_dim:
-            raise ValueError(f"{what}: shape {tuple(x.shape)}, expected [(B,) S, H, {self.head_dim}]")
-        if x.device != like.device:
-            raise ValueError(f"{what} is on {x.device}, expected {like.device}")
-        _same_dtype(x, like, what)
-        if (x.shape[0] if x.dim() == 4 else 1) != B or x.shape[-3] != S:
-            raise ValueError(f"{what}: shape {tuple(x.shape)} does not fit {B} sequences of {S} tokens")
+    def _tensor(self, x, out, B, S, dtype, dev, what):
+        shape = x.shape
+        if len(shape) == 4 and shape[0] == B or len(shape) == 3 and B == 1:
+            good = shape[-3] == S and shape[-1] == self.head_dim
+        else:
+            good = False
+        if not good:
+            raise ValueError(f"{what}: shape {tuple(shape)} does not fit {B} sequences of {S} tokens with heads of {self.head_dim}")
+        if x.dtype is not dtype or x.get_device() != dev:
+            _differs(x, tuple(shape), dtype, dev, what)
         if out is None:
             out = x
-        elif out.shape != x.shape or out.device != x.device:
-            raise ValueError(f"{what}_out: shape {tuple(out.shape)} on {out.device}, expected {tuple(x.shape)} on {x.device}")
-        _same_dtype(out, x, what + "_out")
-        if x.stride(-1) != 1 or out.stride(-1) != 1:
+        elif out.shape != shape or out.dtype is not dtype or out.get_device() != dev:
+            _differs(out, tuple(shape), dtype, dev, what + "_out")
+        st, so = x.stride(), out.stride()
+        if st[-1] != 1 or so[-1] != 1:
             raise ValueError(f"{what}: the elements of a head must be contiguous")
-        b = (lambda t: t.stride(0)) if x.dim() == 4 else (lambda t: 0)
-        return RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[-2], (b(x), x.stride(-3), x.stride(-2)),
-                          (b(out), out.stride(-3), out.stride(-2))), out
+        if len(shape) == 3:
+            st, so = (0, *st), (0, *so)
+        return _ROPE_TENSOR.pack(x.data_ptr(), out.data_ptr(), shape[-2], st[0], st[1], st[2], so[0], so[1], so[2]), out
 
     def apply(self, q, pos, k=None, q_out=None, k_out=None, inverse=False, stream=None):
         """Rotate q and k ([S, H, D] or [B, S, H, D], any strides between heads,
         tokens and sequences; bf16, fp16 or fp32) into q_out and k_out (None: in
         place); ``inverse`` turns back, which is the gradient.  pos is int32,
-        int64 or fp32.  Returns q's output, or both."""
+        int64 or fp32: [S, axes] (shared), [B * S, axes] or [B, S, axes].
+        Returns q's output, or both."""
         kind = _dtype(q, (BF16, FP16, FP32), "q")
-        if q.dim() not in (3, 4):
-            raise ValueError(f"q: shape {tuple(q.shape)}, expected [(B,) S, H, {self.head_dim}]")
-        B, S = (q.shape[0] if q.dim() == 4 else 1), q.shape[-3]
-        tq, q_out = self._tensor(q, q_out, B, S, q, "q")
-        tk = None
+        shape = q.shape
+        if len(shape) not in (3, 4):
+            raise ValueError(f"q: shape {tuple(shape)}, expected [(B,) S, H, {self.head_dim}]")
+        B, S = (shape[0] if len(shape) == 4 else 1), shape[-3]
+        dtype, dev, tk = q.dtype, q.get_device(), None
+        tq, q_out = self._tensor(q, q_out, B, S, dtype, dev, "q")
         if k is not None:
-            tk, k_out = self._tensor(k, k_out, B, S, q, "k")
-        p = self._positions(pos, B, S, q)
-        _check(_run_on(q, stream, self._lib.svdq_rope_apply, self.handle, kind, B, S, ctypes.byref(p), ctypes.byref(tq),
-                       None if tk is None else ctypes.byref(tk), 1 if inverse else 0), "svdq_rope_apply")
+            tk, k_out = self._tensor(k, k_out, B, S, dtype, dev, "k")
+        p = self._positions(pos, B, S, dev)
+        code = _run_on(dev, stream, self._lib.svdq_rope_apply, self.handle, kind, B, S, p, tq, tk, 1 if inverse else 0)
+        if code:
+            raise SvdqError(code, "svdq_rope_apply")
         return q_out if k is None else (q_out, k_out)
 
     def table(self, pos, table, stream=None):
@@ -641,9 +664,9 @@ class RopeAxes:
         S = pos.shape[0]
         if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() != S * sum(self.axis_dims):
             raise ValueError(f"table: expected {S * sum(self.axis_dims)} contiguous fp32 elements")
-        p = self._positions(pos, 1, S, table)
-        _check(_run_on(pos, stream, self._lib.svdq_rope_table, self.handle, 1, S, ctypes.byref(p), table.data_ptr()),
-               "svdq_rope_table")
+        dev = table.get_device()
+        p = self._positions(pos, 1, S, dev)
+        _check(_run_on(dev, stream, self._lib.svdq_rope_table, self.handle, 1, S, p, table.data_ptr()), "svdq_rope_table")
         return table
 
     def close(self) -> None:

@@ -2,6 +2,7 @@
 host before any device work: on a machine without a GPU a valid call ends with
 SVDQ_ERR_UNSUPPORTED_DEVICE, every refusal before that."""
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -209,3 +210,17 @@ def test_rope_python_load_and_table_checks():
         r.table(torch.zeros(6, 2, dtype=torch.int32), torch.zeros(6, 32))
     r.close()
     r.close()
+
+
+def test_packed_layouts():
+    """The struct formats of the binding are the C structs."""
+    for fmt, cls in ((svdq._DENSE, svdq.DenseDesc), (svdq._RMS8, svdq.Rms8Desc), (svdq._ROPE_POS, svdq.RopePositions),
+                     (svdq._ROPE_TENSOR, svdq.RopeTensor)):
+        assert fmt.size == ctypes.sizeof(cls)
+        flat = []
+        for name, t in cls._fields_:
+            flat += [(getattr(cls, name).offset + 8 * i) for i in range(3)] if t is ctypes.c_int64 * 3 else [getattr(cls, name).offset]
+        marks = list(range(1, len(flat) + 1))
+        raw = fmt.pack(*marks)
+        for at, m in zip(flat, marks):
+            assert raw[at] == m or raw[at:at + 4] == struct.pack("f", m)
