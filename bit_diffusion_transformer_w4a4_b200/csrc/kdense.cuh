@@ -41,6 +41,7 @@ struct DenseParams {
   int kblk;               // 128-byte k-blocks
   int num_f, num_t;       // feature and token tiles
   int act;
+  int paired;             // stores and residual loads of two features (see dense_store)
   int* err;               // or null
   uint64_t timeout_ns;
 };
@@ -80,16 +81,25 @@ __device__ __forceinline__ void dense_mma(uint32_t d, uint64_t a, uint64_t b, ui
 // ------------------------------------------------------------------ epilogue
 // What a lane keeps of its feature n for a whole tile.
 struct DenseLane {
-  bool on;        // n < N
+  bool on;          // n < N
   float sw, bias;
+  float gate;       // of gate row g, which serves the tokens before gate_end
+  int g, gate_end;
 };
 
 template <int OUT>
-__device__ __forceinline__ DenseLane dense_lane(const DenseParams& p, int n) {
+__device__ __forceinline__ DenseLane dense_lane(const DenseParams& p, int n, int m0) {
   DenseLane l;
   l.on = n < p.N;
   l.sw = l.on && p.sw ? __ldg(p.sw + n) : 1.f;
   l.bias = l.on && p.bias ? to_f32<OUT>(__ldg(p.bias + n)) : 0.f;
+  l.gate = 0.f;
+  l.g = l.gate_end = 0;
+  if (p.gate && m0 < p.M) {
+    l.g = m0 / p.gate_rows;
+    l.gate_end = (l.g + 1) * p.gate_rows;
+    if (l.on) l.gate = to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>(l.g) * p.ldg + n));
+  }
   return l;
 }
 
@@ -106,70 +116,120 @@ __device__ __forceinline__ uint64_t silu2(uint64_t x) {
   return f2_mul(x, f2_pack(r0, r1));
 }
 
-// The residual of NC tokens m0 .. of feature n; rows beyond M give 0.
-template <int OUT, int NC>
-__device__ __forceinline__ void dense_residual(const DenseParams& p, const DenseLane& l, int m0, int n, uint16_t* r) {
-  const uint16_t* src = p.res + static_cast<int64_t>(m0) * p.ldr + n;
+// gate * act(s_a s_w acc + bias) of NC accumulator columns (tokens m0 ..) of
+// feature n, in pairs of tokens.  sa: the tokens' scales (8-bit kinds; 8-byte
+// aligned), or null.
+template <int KIND, int OUT, int NC>
+__device__ __forceinline__ void dense_math(const DenseParams& p, DenseLane& l, int m0, int n, const uint32_t* acc,
+                                           const float* sa, uint64_t* x) {
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    r[j] = l.on && m0 + j < p.M ? *src : static_cast<uint16_t>(0);
-    src += p.ldr;
+  for (int i = 0; i < NC / 2; ++i)
+    x[i] = KIND == DK_INT8 ? f2_pack(static_cast<float>(static_cast<int>(acc[2 * i])),
+                                     static_cast<float>(static_cast<int>(acc[2 * i + 1])))
+                           : f2_pack(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
+  const uint64_t b2 = f2_pack(l.bias, l.bias);
+  if constexpr (KIND != DK_F16) {
+    const uint64_t w2 = f2_pack(l.sw, l.sw);
+    if (sa) {
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) x[i] = f2_mul(x[i], *reinterpret_cast<const uint64_t*>(sa + 2 * i));
+    }
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) x[i] = f2_fma(x[i], w2, b2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) x[i] = f2_add(x[i], b2);
+  }
+  if (p.act == DENSE_GELU) {
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) x[i] = gelu_tanh2(x[i]);
+  } else if (p.act == DENSE_SILU) {
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) x[i] = silu2(x[i]);
+  }
+  if (p.gate) {
+    if (m0 + NC <= l.gate_end || p.M <= l.gate_end) {  // one gate row for all
+      const uint64_t g2 = f2_pack(l.gate, l.gate);
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) x[i] = f2_mul(x[i], g2);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        if (m0 + j >= l.gate_end && m0 + j < p.M) {
+          ++l.g;
+          l.gate_end += p.gate_rows;
+          if (l.on) l.gate = to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>(l.g) * p.ldg + n));
+        }
+        x[j / 2] = j % 2 ? f2_pack(f2_lo(x[j / 2]), f2_hi(x[j / 2]) * l.gate)
+                         : f2_pack(f2_lo(x[j / 2]) * l.gate, f2_hi(x[j / 2]));
+      }
+    }
   }
 }
 
-// NC accumulator columns (tokens m0 ..) of feature n -> Y.
-template <int KIND, int OUT, int NC>
-__device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLane& l, int m0, int n,
-                                            const uint32_t* acc, const uint16_t* r) {
-  float v[NC];
+// Stores.  In the plain form a lane owns its feature's column of Y: 2 bytes a
+// store, 64 contiguous bytes a warp, any alignment.  In the paired form
+// (p.paired: N and the row distances even, Y and the residual 4-byte aligned)
+// lanes 2i and 2i + 1 first exchange values, so that the even lane holds both
+// features for token j and the odd one both for token j + 1: half the loads
+// and stores, and half the registers of a prefetched residual.
+//
+// dense_residual: the residual of NC tokens m0 .. in the form that
+// dense_store takes, one 32-bit word per token pair (paired) or per token.
+template <int OUT, int NC, bool PAIRED>
+__device__ __forceinline__ void dense_residual(const DenseParams& p, const DenseLane& l, int m0, int n, uint32_t* r) {
+  if constexpr (PAIRED) {
+    const int odd = n & 1;
+    const uint16_t* src = p.res + static_cast<int64_t>(m0 + odd) * p.ldr + (n - odd);
 #pragma unroll
-  for (int j = 0; j < NC; ++j)
-    v[j] = KIND == DK_INT8 ? static_cast<float>(static_cast<int>(acc[j])) : __uint_as_float(acc[j]);
-  if constexpr (KIND != DK_F16) {
-    if (p.sa) {
-#pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] *= l.sw * (m0 + j < p.M ? __ldg(p.sa + m0 + j) : 0.f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] *= l.sw;
+    for (int i = 0; i < NC / 2; ++i) {
+      r[i] = l.on && m0 + odd + 2 * i < p.M ? *reinterpret_cast<const uint32_t*>(src) : 0u;
+      src += 2 * p.ldr;
     }
-  }
-#pragma unroll
-  for (int j = 0; j < NC; ++j) v[j] += l.bias;
-  if (p.act == DENSE_GELU) {
-    gelu_tanh_pairs<NC / 2>(v);
-  } else if (p.act == DENSE_SILU) {
-#pragma unroll
-    for (int j = 0; j < NC; j += 2) {
-      const uint64_t s = silu2(f2_pack(v[j], v[j + 1]));
-      v[j] = f2_lo(s);
-      v[j + 1] = f2_hi(s);
-    }
-  }
-  if (p.gate && l.on) {
-    int g = m0 / p.gate_rows, left = (g + 1) * p.gate_rows - m0;  // tokens left of this gate row
-    const uint16_t* src = p.gate + static_cast<int64_t>(g) * p.ldg + n;
-    float gv = m0 < p.M ? to_f32<OUT>(__ldg(src)) : 0.f;
+  } else {
+    const uint16_t* src = p.res + static_cast<int64_t>(m0) * p.ldr + n;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      if (left == 0) {
-        left = p.gate_rows;
-        src += p.ldg;
-        if (m0 + j < p.M) gv = to_f32<OUT>(__ldg(src));
-      }
-      --left;
-      v[j] *= gv;
+      r[j] = l.on && m0 + j < p.M ? *src : 0u;
+      src += p.ldr;
     }
   }
-  if (p.res) {
+}
+
+template <int OUT>
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
+  if constexpr (OUT == DT_BF16) return pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int OUT, int NC, bool PAIRED>
+__device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLane& l, int m0, int n, const uint64_t* x,
+                                            const uint32_t* r) {
+  if constexpr (PAIRED) {
+    const int odd = n & 1;
+    uint16_t* dst = p.y + static_cast<int64_t>(m0 + odd) * p.ldy + (n - odd);
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] += to_f32<OUT>(r[j]);
-  }
-  uint16_t* dst = p.y + static_cast<int64_t>(m0) * p.ldy + n;
+    for (int i = 0; i < NC / 2; ++i) {
+      const float lo = f2_lo(x[i]), hi = f2_hi(x[i]);
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+      float a = odd ? got : lo, b = odd ? hi : got;
+      if (p.res) {
+        a += to_f32<OUT>(static_cast<uint16_t>(r[i]));
+        b += to_f32<OUT>(static_cast<uint16_t>(r[i] >> 16));
+      }
+      if (l.on && m0 + odd + 2 * i < p.M) *reinterpret_cast<uint32_t*>(dst) = pack_out<OUT>(a, b);
+      dst += 2 * p.ldy;
+    }
+  } else {
+    uint16_t* dst = p.y + static_cast<int64_t>(m0) * p.ldy + n;
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if (l.on && m0 + j < p.M) *dst = from_f32<OUT>(v[j]);
-    dst += p.ldy;
+    for (int j = 0; j < NC; ++j) {
+      float v = j % 2 ? f2_hi(x[j / 2]) : f2_lo(x[j / 2]);
+      if (p.res) v += to_f32<OUT>(static_cast<uint16_t>(r[j]));
+      if (l.on && m0 + j < p.M) *dst = from_f32<OUT>(v);
+      dst += p.ldy;
+    }
   }
 }
 
@@ -179,9 +239,11 @@ __device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLan
 // tile, the leader issues the pair's MMAs (M = 256), and each SM accumulates
 // its 128 features x BN tokens.  Persistent over tiles; two accumulators in
 // tensor memory, so the epilogue of one tile runs under the MMAs of the next.
-// Warps: 0 TMA, 1 MMA and tensor memory, 2-3 idle, 4-11 epilogue.
-constexpr int DP_THREADS = 384;
-constexpr int DP_EPI_WARPS = 8;
+// Warps: 0 TMA, 1 MMA and tensor memory, 2-3 idle, 4-19 epilogue: each of the
+// 16 takes 32 features x BN / 4 tokens.  Their loads for a tile (scales,
+// residual) go out before they wait for its accumulator.
+constexpr int DP_THREADS = 640;
+constexpr int DP_EPI_WARPS = 16;
 
 template <int BN>
 struct DensePairSmem {
@@ -191,7 +253,8 @@ struct DensePairSmem {
   static constexpr int STAGES = BN == 256 ? 6 : 8;
   static constexpr uint32_t TX = 2 * STAGE;
   static constexpr int BAR_OFF = STAGES * STAGE;
-  static constexpr int TOTAL = BAR_OFF + 256 + 1024;
+  static constexpr int SA_OFF = BAR_OFF + 256;              // [16 warps][BN / 4] token scales
+  static constexpr int TOTAL = SA_OFF + DP_EPI_WARPS * BN + 1024;
   static_assert(TOTAL <= 232448, "shared memory per CTA");
 };
 
@@ -320,37 +383,58 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     }
   } else if (warp >= 4) {
     const int e = warp - 4;
+    constexpr int CW = BN / 4;           // tokens of this warp
     const int q = warp & 3;              // tensor-memory lane group of this warp
-    const int c0 = (e >> 2) * (BN / 2);  // its half of the tokens
+    const int c0 = (e >> 2) * CW;
     const uint32_t acc_empty0 = mapa_shared(bar_acc_empty, 0);
+    float* sa = reinterpret_cast<float*>(smem + S::SA_OFF) + e * CW;
     for (int tile = cid, j = 0; tile < num_tiles; tile += nclu, ++j) {
       int ft, tt;
       dense_tile(p, tile, ft, tt);
       const int ac = j & 1;
       const int n = ft * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const int m0 = tt * BN + c0;
-      const DenseLane l = dense_lane<OUT>(p, n);
-      uint16_t r[2][16];
-      if (p.res) dense_residual<OUT, 16>(p, l, m0, n, r[0]);
-      if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
-      tc_fence_after();
+      DenseLane l = dense_lane<OUT>(p, n, m0);
+      if (KIND != DK_F16 && p.sa) {
+        __syncwarp();  // the previous tile's scales have been read
+        for (int i = lane; i < CW; i += 32) sa[i] = m0 + i < p.M ? __ldg(p.sa + m0 + i) : 0.f;
+        __syncwarp();
+      }
+      const float* sc = KIND != DK_F16 && p.sa ? sa : nullptr;
       const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + ac * 256 + c0;
-#pragma unroll 1
-      for (int cc = 0; cc < BN / 2; cc += 32) {
+      auto acc_read = [&] {  // this warp has read its part of the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * ac);
+      };
+      if (p.paired) {
+        uint32_t r[CW / 2];
+        if (p.res) dense_residual<OUT, CW, true>(p, l, m0, n, r);
+        if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
+        tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = cc + 16 * h;
+        for (int c = 0; c < CW; c += 16) {
           uint32_t v[16];
+          uint64_t x[8];
           tmem_ld_x16(ta + c, v);
-          // the next columns' residual is on its way while these are stored
-          if (p.res && c + 16 < BN / 2) dense_residual<OUT, 16>(p, l, m0 + c + 16, n, r[1 - h]);
           tmem_ld_wait();
-          if (c + 16 == BN / 2) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * ac);
-          }
-          if (m0 + c < p.M) dense_store<KIND, OUT, 16>(p, l, m0 + c, n, v, r[h]);
+          if (c + 16 == CW) acc_read();
+          dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+          dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r + c / 2);
+        }
+      } else {
+        if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < CW; c += 16) {
+          uint32_t v[16], r[16];
+          uint64_t x[8];
+          tmem_ld_x16(ta + c, v);
+          if (p.res) dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
+          tmem_ld_wait();
+          if (c + 16 == CW) acc_read();
+          dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+          dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
         }
       }
     }
@@ -379,7 +463,8 @@ struct DenseSoloSmem {
   static constexpr int STAGE = W_BYTES + A_BYTES;
   static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 3;  // two CTAs fit an SM
   static constexpr int BAR_OFF = STAGES * STAGE;
-  static constexpr int TOTAL = BAR_OFF + 256 + 1024;
+  static constexpr int SA_OFF = BAR_OFF + 256;                    // [BN] token scales
+  static constexpr int TOTAL = SA_OFF + BN * 4 + 1024;
   static_assert(128 * BN * 4 <= BAR_OFF, "the partial tile fits the stages");
   static_assert(2 * TOTAL <= 232448, "shared memory of two CTAs");
 };
@@ -491,8 +576,14 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
   const int valid = min(BN, p.M - m0);  // tokens of the tile
   bool ok = true;
   DenseLane l = {};
+  float* sa = reinterpret_cast<float*>(smem + S::SA_OFF);
+  const float* sc = KIND != DK_F16 && p.sa ? sa : nullptr;
+  if (sc) {
+    for (int i = threadIdx.x; i < BN; i += DS_THREADS) sa[i] = m0 + i < p.M ? __ldg(p.sa + m0 + i) : 0.f;
+    __syncthreads();
+  }
   if (warp >= 2) {
-    l = dense_lane<OUT>(p, n);
+    l = dense_lane<OUT>(p, n, m0);
     ok = __all_sync(0xffffffffu, wait_bounded(bar_acc, 0, guard, 0x313, 32));
     tc_fence_after();
     const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -500,12 +591,17 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
       if (ok) {
 #pragma unroll 1
         for (int c = 0; c < valid; c += 16) {
-          uint32_t v[16];
-          uint16_t r[16];
+          uint32_t v[16], r[16];
+          uint64_t x[8];
           tmem_ld_x16(ta + c, v);
-          if (p.res) dense_residual<OUT, 16>(p, l, m0 + c, n, r);
+          if (p.res) {
+            if (p.paired) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
+            else dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
+          }
           tmem_ld_wait();
-          dense_store<KIND, OUT, 16>(p, l, m0 + c, n, v, r);
+          dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+          if (p.paired) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
+          else dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
         }
       }
     } else if (ok) {
@@ -527,29 +623,31 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
     if (warp >= 2 && ok) {
       const int per = 2 * ((valid + 2 * split - 1) / (2 * split));  // even: two tokens at a time
       const int c1 = min(valid, (rank + 1) * per);
+      if (p.gate) l = dense_lane<OUT>(p, n, m0 + rank * per);
       for (int c = rank * per; c < c1; c += 2) {
-        uint32_t v[2];
-        uint16_t r[2];
-        if (p.res) dense_residual<OUT, 2>(p, l, m0 + c, n, r);
+        uint32_t v[2], r[2];
+        uint64_t x[1];
+        if (p.res) dense_residual<OUT, 2, false>(p, l, m0 + c, n, r);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t at = sbase + ((c + j) * 128 + f) * 4;
-          uint32_t x[8];
+          uint32_t w[8];
 #pragma unroll
-          for (int o = 0; o < 8; ++o) x[o] = o < split ? ld_cluster_u32(mapa_shared(at, o)) : 0u;
+          for (int o = 0; o < 8; ++o) w[o] = o < split ? ld_cluster_u32(mapa_shared(at, o)) : 0u;
           if constexpr (KIND == DK_INT8) {
             int a = 0;
 #pragma unroll
-            for (int o = 0; o < 8; ++o) a += static_cast<int>(x[o]);
+            for (int o = 0; o < 8; ++o) a += static_cast<int>(w[o]);
             v[j] = static_cast<uint32_t>(a);
           } else {
             float a = 0.f;
 #pragma unroll
-            for (int o = 0; o < 8; ++o) a += __uint_as_float(x[o]);
+            for (int o = 0; o < 8; ++o) a += __uint_as_float(w[o]);
             v[j] = __float_as_uint(a);
           }
         }
-        dense_store<KIND, OUT, 2>(p, l, m0 + c, n, v, r);
+        dense_math<KIND, OUT, 2>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+        dense_store<OUT, 2, false>(p, l, m0 + c, n, x, r);
       }
     }
     cluster_sync();  // no CTA leaves while its partial tile may be read

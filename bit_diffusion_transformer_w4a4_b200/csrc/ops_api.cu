@@ -341,6 +341,8 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
   c.p.N = static_cast<int>(N);
   c.p.kblk = static_cast<int>(cdiv(K * es, 128));
   c.p.act = static_cast<int>(d->act);
+  c.p.paired = N % 2 == 0 && aligned(d->y, 4) && (M == 1 || d->ldy % 2 == 0) &&
+               (!d->residual || (aligned(d->residual, 4) && (M == 1 || d->ldr % 2 == 0)));
   c.p.err = d->device_error;
   c.p.timeout_ns = kDefaultTimeoutNs;
   const bool bf = d->out == SVDQ_BF16;
