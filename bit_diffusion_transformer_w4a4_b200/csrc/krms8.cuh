@@ -13,14 +13,19 @@
 // which stays in registers between the pass and the conversion.
 //
 // Bound by memory: x and the residual are read once, h, the codes and the
-// scales written once.  A CTA owns one row; its two statistics cross the
-// warps through shared memory behind a single barrier, and the CTAs that
-// share an SM hide each other's barriers and loads.
+// scales written once.  The two statistics of a row cross the warps of its
+// CTA through shared memory behind a single barrier.  Two kernels:
+//   rms8_kernel       one CTA per row, any alignment: the row goes straight
+//                     into registers
+//   rms8_ring_kernel  many 16-byte aligned rows: persistent CTAs whose next
+//                     rows are always on their way into a ring in shared
+//                     memory (bulk copies), so that loads do not pause while
+//                     a row is reduced and converted
 #pragma once
 
 #include <cuda_fp8.h>
 
-#include "ptx.cuh"
+#include "kg_common.cuh"
 
 namespace svdq {
 
@@ -64,6 +69,47 @@ struct Pack {
   }
 };
 
+// Elements 2i and 2i + 1 as a pair of fp32, and back.
+template <int DT, int VEC>
+__device__ __forceinline__ uint64_t get2(const Pack<DT, VEC>& a, int i) {
+  if constexpr (DT == DT_FP32) {
+    return f2_pack(a.e[2 * i], a.e[2 * i + 1]);
+  } else {
+    const uint32_t u = reinterpret_cast<const uint32_t*>(a.e)[i];
+    if constexpr (DT == DT_BF16) return f2_pack(bf16lo(u), bf16hi(u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    return f2_pack(f.x, f.y);
+  }
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void set2(Pack<DT, VEC>& a, int i, uint64_t v) {
+  if constexpr (DT == DT_FP32) {
+    a.e[2 * i] = f2_lo(v);
+    a.e[2 * i + 1] = f2_hi(v);
+  } else if constexpr (DT == DT_BF16) {
+    reinterpret_cast<uint32_t*>(a.e)[i] = pack_bf16x2(f2_lo(v), f2_hi(v));
+  } else {
+    const __half2 h = __floats2half2_rn(f2_lo(v), f2_hi(v));
+    reinterpret_cast<uint32_t*>(a.e)[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+// a <- round(a + b)
+template <int DT, int VEC>
+__device__ __forceinline__ void add_to(Pack<DT, VEC>& a, const Pack<DT, VEC>& b) {
+  if constexpr (VEC == 1) {
+    a.e[0] = from_f32<DT>(to_f32<DT>(a.e[0]) + to_f32<DT>(b.e[0]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) set2(a, i, f2_add(get2(a, i), get2(b, i)));
+  }
+}
+// The larger of m, |a| and |b|; NaN if any is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+
 struct RmsParams {
   const void* x;
   const void* res;      // or null
@@ -72,7 +118,8 @@ struct RmsParams {
   uint8_t* codes;
   float* scales;
   int64_t ldx, ldr, ldh, ldw, ldc;  // elements
-  int64_t w_rows;       // rows of x that share a row of w
+  int64_t w_rows;       // rows of x that share a row of w (0: all)
+  float inv_K;
   int K;
   int norm, int8;
   float eps;
@@ -100,9 +147,119 @@ __device__ __forceinline__ float block_sum(float v, float* red, int nw) {
   return v;
 }
 
+// The row's statistics, joined over the CTA in a fixed order; the barrier
+// also ends the warps' reads of the row.  The maximum is not negative, so its
+// bits are ordered like its values, NaN above infinity.
+struct RmsStats {
+  uint64_t ss = 0;   // two partial sums of squares
+  float top = 0.f;   // max |t|
+};
+__device__ __forceinline__ void rms8_join(const RmsStats& st, float& ss, uint32_t& top, float* red_s, uint32_t* red_m, int nw) {
+  top = __reduce_max_sync(0xffffffffu, __float_as_uint(st.top));
+  ss = f2_lo(st.ss) + f2_hi(st.ss);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (nw > 1) {
+    const int l = threadIdx.x & 31;
+    if (l == 0) {
+      red_s[threadIdx.x >> 5] = ss;
+      red_m[threadIdx.x >> 5] = top;
+    }
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, l < nw ? red_m[l] : 0u);
+    ss = l < nw ? red_s[l] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  } else {
+    __syncwarp();
+  }
+}
+
+// t of elements 2i, 2i + 1 (VEC = 1: of the element, with 0).
+template <int DT, int VEC>
+__device__ __forceinline__ uint64_t rms8_t(const RmsParams& p, const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, int i) {
+  if constexpr (VEC == 1) {
+    const float v = to_f32<DT>(a.e[0]);
+    return f2_pack(p.w ? v * to_f32<DT>(g.e[0]) : v, 0.f);
+  } else {
+    const uint64_t v = get2(a, i);
+    return p.w ? f2_mul(v, get2(g, i)) : v;
+  }
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void rms8_stats(const RmsParams& p, const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, RmsStats& st) {
+  if (p.norm) {
+    if constexpr (VEC == 1) {
+      const uint64_t v = f2_pack(to_f32<DT>(a.e[0]), 0.f);
+      st.ss = f2_fma(v, v, st.ss);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        const uint64_t v = get2(a, i);
+        st.ss = f2_fma(v, v, st.ss);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i) {
+    const uint64_t t = rms8_t(p, a, g, i);
+    st.top = max_abs(st.top, f2_lo(t), f2_hi(t));
+  }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ float rms8_squares_down(const Pack<DT, VEC>& a, float s) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const float v = to_f32<DT>(a.e[i]) * kRmsDown;
+    s = fmaf(v, v, s);
+  }
+  return s;
+}
+
+// The factor from t to the codes; thread 0 writes the row's scale.  `again`:
+// the row's squares summed scaled by kRmsDown (called by the whole CTA or not
+// at all).
+template <class F>
+__device__ __forceinline__ float rms8_scale(const RmsParams& p, int64_t row, float ss, uint32_t top, F again) {
+  const float amax = __uint_as_float(top);
+  const bool finite = top < 0x7F800000u;
+  const bool live = finite && amax >= kRmsTiny;
+  const float lim = p.int8 ? 127.f : 448.f;
+  float s2 = 0.f;
+  const bool down = p.norm && finite && !(ss < INFINITY);
+  if (down) s2 = again();
+  if (threadIdx.x == 0) {
+    float rstd = 1.f;
+    if (p.norm) rstd = down ? kRmsDown / sqrtf(s2 * p.inv_K) : 1.f / sqrtf(fmaf(ss, p.inv_K, p.eps));
+    p.scales[row] = live ? __fdiv_rn(amax * rstd, lim) : finite ? 0.f : __uint_as_float(0x7FC00000u);
+  }
+  return live ? __fdiv_rn(lim, amax) : 0.f;
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ void rms8_codes(const RmsParams& p, const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, float inv,
+                                           uint8_t* out) {
+  const uint64_t inv2 = f2_pack(inv, inv);
+  uint32_t q[(VEC + 3) / 4] = {};
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i) {
+    const uint64_t z = f2_mul(rms8_t(p, a, g, i), inv2);
+    uint32_t two;
+    if (p.int8)  // at most 127 (1 + 2^-23): rounds to at most 127
+      two = (static_cast<uint32_t>(__float2int_rn(f2_lo(z))) & 0xFFu) | (static_cast<uint32_t>(__float2int_rn(f2_hi(z))) & 0xFFu) << 8;
+    else
+      two = __nv_cvt_float2_to_fp8x2(make_float2(f2_lo(z), f2_hi(z)), __NV_SATFINITE, __NV_E4M3);
+    q[i / 2] |= two << (16 * (i % 2));
+  }
+  if constexpr (VEC == 8) *reinterpret_cast<uint2*>(out) = make_uint2(q[0], q[1]);
+  else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(out) = q[0];
+  else out[0] = static_cast<uint8_t>(q[0]);
+}
+
 // CH chunks of VEC elements per thread.
 template <int DT, int VEC, int CH>
-__global__ void __launch_bounds__(1024) rms8_kernel(const RmsParams p) {
+__global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
   using E = typename ElemOf<DT>::type;
   __shared__ float red_s[32];
   __shared__ uint32_t red_m[32];
@@ -114,17 +271,16 @@ __global__ void __launch_bounds__(1024) rms8_kernel(const RmsParams p) {
   const E* x = static_cast<const E*>(p.x) + row * p.ldx;
   const E* r = static_cast<const E*>(p.res) + row * p.ldr;
   E* h = static_cast<E*>(p.h) + row * p.ldh;
-  const E* w = static_cast<const E*>(p.w) + (p.w ? row / p.w_rows * p.ldw : 0);
+  const E* w = static_cast<const E*>(p.w) + (p.w && p.w_rows ? row / p.w_rows * p.ldw : 0);
   uint8_t* codes = p.codes + row * p.ldc;
 
-  float t[CH * VEC];
+  // The row stays packed in registers; t is formed twice (for the maximum and
+  // for the codes) rather than kept, which leaves room for twice the threads.
   Pack<DT, VEC> a[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
     if (k < p.K) a[c].load(x + k);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) t[c * VEC + i] = 0.f;
   }
   if (p.res) {
 #pragma unroll
@@ -133,93 +289,154 @@ __global__ void __launch_bounds__(1024) rms8_kernel(const RmsParams p) {
       if (k < p.K) {
         Pack<DT, VEC> b;
         b.load(r + k);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) a[c].e[i] = from_f32<DT>(to_f32<DT>(a[c].e[i]) + to_f32<DT>(b.e[i]));
+        add_to(a[c], b);
+        if (p.h) a[c].store(h + k);
       }
     }
+  } else if (p.h) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
+      if (k < p.K) a[c].store(h + k);
+    }
   }
-  float ss = 0.f;
-  uint32_t top = 0;  // |t| as bits: ordered like the values, NaN above infinity
+  RmsStats st;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
     if (k < p.K) {
-      if (p.h) a[c].store(h + k);
       Pack<DT, VEC> g;
       if (p.w) g.load_cached(w + k);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float v = to_f32<DT>(a[c].e[i]);
-        ss = fmaf(v, v, ss);
-        const float tv = p.w ? v * to_f32<DT>(g.e[i]) : v;
-        t[c * VEC + i] = tv;
-        top = max(top, __float_as_uint(tv) & 0x7FFFFFFFu);
-      }
+      rms8_stats<DT, VEC>(p, a[c], g, st);
     }
   }
-  top = __reduce_max_sync(0xffffffffu, top);
+  float ss;
+  uint32_t top;
+  rms8_join(st, ss, top, red_s, red_m, nw);
+  const float inv = rms8_scale(p, row, ss, top, [&] {
+    float s2 = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (nw > 1) {
-    if ((threadIdx.x & 31) == 0) {
-      red_s[threadIdx.x >> 5] = ss;
-      red_m[threadIdx.x >> 5] = top;
+    for (int c = 0; c < CH; ++c) {
+      const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
+      if (k < p.K) s2 = rms8_squares_down<DT, VEC>(a[c], s2);
     }
-    __syncthreads();
-    const int l = threadIdx.x & 31;
-    top = __reduce_max_sync(0xffffffffu, l < nw ? red_m[l] : 0u);
-    ss = l < nw ? red_s[l] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  }
-  const float amax = __uint_as_float(top);
-  const bool finite = top < 0x7F800000u;
-  float rstd = 1.f;
-  if (p.norm) {
-    rstd = 1.f / sqrtf(ss / static_cast<float>(p.K) + p.eps);
-    if (finite && !(ss < INFINITY)) {  // the same for the whole CTA
-      float s2 = 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
-        if (k < p.K) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float v = to_f32<DT>(a[c].e[i]) * kRmsDown;
-            s2 = fmaf(v, v, s2);
-          }
-        }
-      }
-      s2 = block_sum(s2, red_s, nw);
-      rstd = kRmsDown / sqrtf(s2 / static_cast<float>(p.K));
-    }
-  }
-  const float lim = p.int8 ? 127.f : 448.f;
-  const bool live = amax >= kRmsTiny;
-  const float inv = live && finite ? __fdiv_rn(lim, amax) : 0.f;
-  if (threadIdx.x == 0)
-    p.scales[row] = finite ? (live ? __fdiv_rn(amax * rstd, lim) : 0.f) : __uint_as_float(0x7FC00000u);
+    return block_sum(s2, red_s, nw);
+  });
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
     if (k >= p.K) continue;
-    uint32_t q[(VEC + 3) / 4] = {};
-    if (p.int8) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i)  // |t inv| <= 127 (1 + 2^-23): rounds to at most 127
-        q[i / 4] |= (static_cast<uint32_t>(__float2int_rn(t[c * VEC + i] * inv)) & 0xFFu) << (8 * (i % 4));
-    } else if constexpr (VEC == 1) {
-      q[0] = __nv_cvt_float_to_fp8(t[c] * inv, __NV_SATFINITE, __NV_E4M3);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; i += 2)
-        q[i / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-                        make_float2(t[c * VEC + i] * inv, t[c * VEC + i + 1] * inv), __NV_SATFINITE, __NV_E4M3))
-                    << (8 * (i % 4));
+    Pack<DT, VEC> g;
+    if (p.w) g.load_cached(w + k);
+    rms8_codes<DT, VEC>(p, a[c], g, inv, codes + k);
+  }
+}
+
+// ------------------------------------------------------------- the ring form
+__device__ int g_rms8_err;  // error word of the bounded waits (this call reports none)
+
+struct RmsRing {
+  int64_t M;
+  int slots;       // rows of the ring
+  int row_bytes;   // K elements
+  uint64_t timeout_ns;
+};
+
+// Shared memory: slots x (x row, residual row), then the barriers.
+template <int DT, int CH>
+__global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const RmsRing g) {
+  using E = typename ElemOf<DT>::type;
+  constexpr int VEC = 16 / sizeof(E);
+  constexpr int SLOTS = 8;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t bars[SLOTS];
+  __shared__ float red_s[2][32];
+  __shared__ uint32_t red_m[2][32];
+  __shared__ int abort_flag;
+  const int nt = blockDim.x, nw = nt >> 5;
+  const uint32_t bar0 = smem_u32(bars);
+  const Guard guard{&g_rms8_err, &abort_flag, g.timeout_ns};
+  const uint32_t slot_bytes = g.row_bytes * (p.res ? 2u : 1u);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < g.slots; ++i) mbar_init(bar0 + 8 * i, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  auto issue = [&](int64_t row, int slot) {  // thread 0
+    const uint32_t dst = smem_u32(ring) + slot * slot_bytes;
+    mbar_expect_tx(bar0 + 8 * slot, slot_bytes);
+    bulk_load(dst, static_cast<const E*>(p.x) + row * p.ldx, g.row_bytes, bar0 + 8 * slot);
+    if (p.res) bulk_load(dst + g.row_bytes, static_cast<const E*>(p.res) + row * p.ldr, g.row_bytes, bar0 + 8 * slot);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < g.slots; ++i) {
+      const int64_t row = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+      if (row < g.M) issue(row, i);
     }
-    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(codes + k) = make_uint2(q[0], q[1]);
-    else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(codes + k) = q[0];
-    else codes[k] = static_cast<uint8_t>(q[0]);
+  Pack<DT, VEC> w[CH];   // the weight row in use
+  int64_t w_end = 0;     // the first row that it does not serve
+  int slot = 0;
+  uint32_t ph = 0;
+  int it = 0;
+  for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x, it ^= 1) {
+    if (p.w && row >= w_end) {
+      const int64_t w_row = p.w_rows ? row / p.w_rows : 0;
+      w_end = p.w_rows ? (w_row + 1) * p.w_rows : g.M;
+      const E* src = static_cast<const E*>(p.w) + w_row * p.ldw;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
+        if (k < p.K) w[c].load_cached(src + k);
+      }
+    }
+    if (!wait_bounded(bar0 + 8 * slot, ph, guard, 0x321)) {
+      if (threadIdx.x == 0)  // the rows on their way land before the CTA leaves
+        drain_loads(bar0, (1u << g.slots) - 1, ph ? (1u << g.slots) - (1u << slot) : (1u << slot) - 1, g.slots, g.timeout_ns);
+      return;
+    }
+    const uint8_t* sx = ring + slot * slot_bytes;
+    Pack<DT, VEC> a[CH];
+    RmsStats st;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
+      if (k < p.K) {
+        a[c].q = *reinterpret_cast<const uint4*>(sx + k * sizeof(E));
+        if (p.res) {
+          Pack<DT, VEC> b;
+          b.q = *reinterpret_cast<const uint4*>(sx + g.row_bytes + k * sizeof(E));
+          add_to(a[c], b);
+        }
+        if (p.h) a[c].store(static_cast<E*>(p.h) + row * p.ldh + k);
+        rms8_stats<DT, VEC>(p, a[c], w[c], st);
+      }
+    }
+    float ss;
+    uint32_t top;
+    rms8_join(st, ss, top, red_s[it], red_m[it], nw);
+    // every thread has read the slot (the join's barrier): the next row in
+    if (threadIdx.x == 0) {
+      const int64_t next = row + static_cast<int64_t>(g.slots) * gridDim.x;
+      if (next < g.M) issue(next, slot);
+    }
+    const float inv = rms8_scale(p, row, ss, top, [&] {
+      float s2 = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
+        if (k < p.K) s2 = rms8_squares_down<DT, VEC>(a[c], s2);
+      }
+      return block_sum(s2, red_s[it], nw);
+    });
+  #pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
+      if (k < p.K) rms8_codes<DT, VEC>(p, a[c], w[c], inv, p.codes + row * p.ldc + k);
+    }
+    if (++slot == g.slots) { slot = 0; ph ^= 1; }
   }
 }
 

@@ -57,14 +57,13 @@ struct RopeParams {
   int pass;                      // elements beyond the rotated span are copied
 };
 
-__device__ __forceinline__ float2 rope_cos_sin(const RopePlan& plan, const RopePos& pos, int64_t b, int64_t s,
-                                               int pair) {
-  const int64_t o = b * pos.sb + s * pos.ss + plan.axis[pair] * pos.sa;
+__device__ __forceinline__ float2 rope_cos_sin(const RopePos& pos, int64_t b, int64_t s, int axis, double f) {
+  const int64_t o = b * pos.sb + s * pos.ss + axis * pos.sa;
   double v;
   if (pos.type == 0) v = static_cast<double>(__ldg(static_cast<const int*>(pos.p) + o));
   else if (pos.type == 1) v = static_cast<double>(__ldg(static_cast<const long long*>(pos.p) + o));
   else v = static_cast<double>(__ldg(static_cast<const float*>(pos.p) + o));
-  const double u = v * plan.f[pair];
+  const double u = v * f;
   const float turn = static_cast<float>(u - 2.0 * rint(0.5 * u));
   float2 cs;
   sincospif(turn, &cs.y, &cs.x);
@@ -75,12 +74,19 @@ __device__ __forceinline__ float2 rope_cos_sin(const RopePlan& plan, const RopeP
 // (VEC / 2 pairs), of the split form two pieces (VEC pairs); the scalar unit
 // is one pair in both.  Units beyond the rotating ones copy one piece.
 template <int DT, int VEC, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_axes_kernel(const __grid_constant__ RopeParams p) {
   using E = typename ElemOf<DT>::type;
   constexpr bool TWO = !INTER || VEC == 1;                   // a unit's pairs span two pieces
   constexpr int NP = TWO ? VEC : VEC / 2;                    // pairs per rotating unit
-  constexpr int HB = 4;
+  constexpr int HB = TWO ? 2 : 4;
   __shared__ float2 cs[ROPE_TOKENS][ROPE_MAX_PAIRS];
+  __shared__ double freq[ROPE_MAX_PAIRS];
+  __shared__ uint8_t axis[ROPE_MAX_PAIRS];
+  if (threadIdx.x < p.plan.pairs) {  // lanes' own indexes into the parameters replay: once per pair, not per angle
+    freq[threadIdx.x] = p.plan.f[threadIdx.x];
+    axis[threadIdx.x] = p.plan.axis[threadIdx.x];
+  }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   const int pairs = p.plan.pairs;
@@ -89,7 +95,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_axes_kernel(const __grid_co
   for (int i = threadIdx.x; i < nt * pairs; i += ROPE_THREADS) {
     const int t = i / pairs, pr = i - t * pairs;
     const int64_t tok = tok0 + t;
-    float2 v = rope_cos_sin(p.plan, p.pos, tok / p.S, tok % p.S, pr);
+    float2 v = rope_cos_sin(p.pos, tok / p.S, tok % p.S, axis[pr], freq[pr]);
     v.y *= p.sign;
     cs[t][pr] = v;
   }
@@ -165,7 +171,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_table_kernel(const __grid_c
   const int64_t i = static_cast<int64_t>(blockIdx.x) * ROPE_THREADS + threadIdx.x;
   const int64_t tok = i / p.plan.pairs;
   if (tok >= p.tokens) return;
-  p.table[i] = rope_cos_sin(p.plan, p.pos, tok / p.S, tok % p.S, static_cast<int>(i - tok * p.plan.pairs));
+  const int pr = static_cast<int>(i - tok * p.plan.pairs);
+  p.table[i] = rope_cos_sin(p.pos, tok / p.S, tok % p.S, p.plan.axis[pr], p.plan.f[pr]);
 }
 
 }  // namespace svdq

@@ -71,6 +71,9 @@ bool overlap(const Region& a, const Region& b) {
 bool same(const Region& a, const Region& b) { return a.p == b.p && (a.ld == b.ld || a.rows == 1); }
 
 // ------------------------------------------------------------------ RMS norm
+constexpr int kRmsSlots = 4;               // rows in flight per CTA of the ring form, at most (at least 2)
+constexpr int kRmsRingMax = 220 * 1024;    // its shared memory
+
 template <int DT, int VEC, int CH>
 svdq_status launch_rms_t(const RmsParams& p, int64_t M, int nt, cudaStream_t st) {
   LaunchCfg lc(dim3(static_cast<unsigned>(M)), dim3(nt), 0, st);
@@ -98,13 +101,51 @@ svdq_status launch_rms_v(const RmsParams& p, int64_t M, int sms, cudaStream_t st
   return SVDQ_ERR_SHAPE;
 }
 
+// Many aligned rows (see rms8_ring_kernel).
+template <int DT, int CH>
+svdq_status launch_rms_ring_t(const RmsParams& p, int64_t M, int sms, int nt, cudaStream_t st) {
+  const int row_bytes = p.K * (DT == DT_FP32 ? 4 : 2);
+  const int slot = row_bytes * (p.res ? 2 : 1);
+  if (svdq_status s = ensure_smem<rms8_ring_kernel<DT, CH>>(kRmsRingMax); s != SVDQ_OK) return s;
+  static std::atomic<int> known{0};  // registers per thread: the same on every device
+  int regs = known.load(std::memory_order_relaxed);
+  if (regs == 0) {
+    cudaFuncAttributes fa;
+    SVDQ_TRY(cudaFuncGetAttributes(&fa, rms8_ring_kernel<DT, CH>));
+    known.store(regs = std::max(16, fa.numRegs), std::memory_order_relaxed);
+  }
+  // resident CTAs by registers (granted per warp in steps of 8 a thread),
+  // threads and two slots each; the shared memory that this leaves makes more slots
+  const int by_regs = 65536 / (static_cast<int>(cdiv(regs, 8) * 8) * nt);
+  const int per_sm = std::max(1, std::min({(227 * 1024) / (2 * slot + 2048), by_regs, 2048 / nt, 32}));
+  const int slots = std::min({kRmsSlots, kRmsRingMax / slot, (227 * 1024 / per_sm - 2048) / slot});
+  RmsRing g{M, slots, row_bytes, kDefaultTimeoutNs};
+  const int smem = slots * slot;
+  LaunchCfg lc(dim3(static_cast<unsigned>(std::min<int64_t>(M, static_cast<int64_t>(sms) * per_sm))), dim3(nt), smem, st);
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_ring_kernel<DT, CH>, p, g));
+  return SVDQ_OK;
+}
+
+template <int DT>
+svdq_status launch_rms_ring(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
+  constexpr int V = DT == DT_FP32 ? 4 : 8;
+  const int64_t pieces = p.K / V;
+  auto threads = [&](int c) { return static_cast<int>(cdiv(cdiv(pieces, c), 32) * 32); };
+  // two pieces a thread for short rows and where an SM has few rows (latency), else four
+  if (threads(2) <= 128 || (M <= 4 * sms && threads(2) <= 512)) return launch_rms_ring_t<DT, 2>(p, M, sms, threads(2), st);
+  return launch_rms_ring_t<DT, 4>(p, M, sms, threads(4), st);
+}
+
 template <int DT>
 svdq_status launch_rms(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
   constexpr int V = DT == DT_FP32 ? 4 : 8;
   const bool vec = p.K % V == 0 && aligned16(p.x) && p.ldx % V == 0 && (!p.res || (aligned16(p.res) && p.ldr % V == 0)) &&
                    (!p.h || (aligned16(p.h) && p.ldh % V == 0)) && (!p.w || (aligned16(p.w) && p.ldw % V == 0)) &&
                    aligned(p.codes, V) && p.ldc % V == 0;
-  return vec ? launch_rms_v<DT, V>(p, M, sms, st) : launch_rms_v<DT, 1>(p, M, sms, st);
+  if (!vec) return launch_rms_v<DT, 1>(p, M, sms, st);
+  const int64_t slot = static_cast<int64_t>(p.K) * (DT == DT_FP32 ? 4 : 2) * (p.res ? 2 : 1);
+  if (M > sms && 2 * slot <= kRmsRingMax && p.K / V <= 4 * 512) return launch_rms_ring<DT>(p, M, sms, st);
+  return launch_rms_v<DT, V>(p, M, sms, st);
 }
 
 // --------------------------------------------------------------------- rotary
@@ -392,7 +433,8 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
   p.ldh = d->ldh;
   p.ldw = d->ldw;
   p.ldc = d->ldc;
-  p.w_rows = d->weight ? d->weight_rows : 1;
+  p.w_rows = d->weight && d->weight_rows < M ? d->weight_rows : 0;
+  p.inv_K = 1.0f / static_cast<float>(K);
   p.K = static_cast<int>(K);
   p.norm = d->norm;
   p.int8 = d->out == SVDQ_INT8;
