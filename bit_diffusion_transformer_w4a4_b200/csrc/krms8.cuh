@@ -176,17 +176,17 @@ __device__ __forceinline__ void rms8_join(const RmsStats& st, float& ss, uint32_
 }
 
 // t of elements 2i, 2i + 1 (VEC = 1: of the element, with 0).
-template <int DT, int VEC>
-__device__ __forceinline__ uint64_t rms8_t(const RmsParams& p, const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, int i) {
+template <int DT, int VEC, bool HW>
+__device__ __forceinline__ uint64_t rms8_t(const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, int i) {
   if constexpr (VEC == 1) {
     const float v = to_f32<DT>(a.e[0]);
-    return f2_pack(p.w ? v * to_f32<DT>(g.e[0]) : v, 0.f);
+    return f2_pack(HW ? v * to_f32<DT>(g.e[0]) : v, 0.f);
   } else {
     const uint64_t v = get2(a, i);
-    return p.w ? f2_mul(v, get2(g, i)) : v;
+    return HW ? f2_mul(v, get2(g, i)) : v;
   }
 }
-template <int DT, int VEC>
+template <int DT, int VEC, bool HW>
 __device__ __forceinline__ void rms8_stats(const RmsParams& p, const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, RmsStats& st) {
   if (p.norm) {
     if constexpr (VEC == 1) {
@@ -202,7 +202,7 @@ __device__ __forceinline__ void rms8_stats(const RmsParams& p, const Pack<DT, VE
   }
 #pragma unroll
   for (int i = 0; i < (VEC + 1) / 2; ++i) {
-    const uint64_t t = rms8_t(p, a, g, i);
+    const uint64_t t = rms8_t<DT, VEC, HW>(a, g, i);
     st.top = max_abs(st.top, f2_lo(t), f2_hi(t));
   }
 }
@@ -237,16 +237,16 @@ __device__ __forceinline__ float rms8_scale(const RmsParams& p, int64_t row, flo
   return live ? __fdiv_rn(lim, amax) : 0.f;
 }
 
-template <int DT, int VEC>
-__device__ __forceinline__ void rms8_codes(const RmsParams& p, const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, float inv,
+template <int DT, int VEC, bool HW, bool I8>
+__device__ __forceinline__ void rms8_codes(const Pack<DT, VEC>& a, const Pack<DT, VEC>& g, float inv,
                                            uint8_t* out) {
   const uint64_t inv2 = f2_pack(inv, inv);
   uint32_t q[(VEC + 3) / 4] = {};
 #pragma unroll
   for (int i = 0; i < (VEC + 1) / 2; ++i) {
-    const uint64_t z = f2_mul(rms8_t(p, a, g, i), inv2);
+    const uint64_t z = f2_mul(rms8_t<DT, VEC, HW>(a, g, i), inv2);
     uint32_t two;
-    if (p.int8)  // at most 127 (1 + 2^-23): rounds to at most 127
+    if constexpr (I8)  // at most 127 (1 + 2^-23): rounds to at most 127
       two = (static_cast<uint32_t>(__float2int_rn(f2_lo(z))) & 0xFFu) | (static_cast<uint32_t>(__float2int_rn(f2_hi(z))) & 0xFFu) << 8;
     else
       two = __nv_cvt_float2_to_fp8x2(make_float2(f2_lo(z), f2_hi(z)), __NV_SATFINITE, __NV_E4M3);
@@ -257,8 +257,8 @@ __device__ __forceinline__ void rms8_codes(const RmsParams& p, const Pack<DT, VE
   else out[0] = static_cast<uint8_t>(q[0]);
 }
 
-// CH chunks of VEC elements per thread.
-template <int DT, int VEC, int CH>
+// CH chunks of VEC elements per thread; HW: with a weight; I8: INT8 codes.
+template <int DT, int VEC, int CH, bool HW, bool I8>
 __global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
   using E = typename ElemOf<DT>::type;
   __shared__ float red_s[32];
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
   const E* x = static_cast<const E*>(p.x) + row * p.ldx;
   const E* r = static_cast<const E*>(p.res) + row * p.ldr;
   E* h = static_cast<E*>(p.h) + row * p.ldh;
-  const E* w = static_cast<const E*>(p.w) + (p.w && p.w_rows ? row / p.w_rows * p.ldw : 0);
+  const E* w = static_cast<const E*>(p.w) + (HW && p.w_rows ? row / p.w_rows * p.ldw : 0);
   uint8_t* codes = p.codes + row * p.ldc;
 
   // The row stays packed in registers; t is formed twice (for the maximum and
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
     const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
     if (k < p.K) {
       Pack<DT, VEC> g;
-      if (p.w) g.load_cached(w + k);
-      rms8_stats<DT, VEC>(p, a[c], g, st);
+      if (HW) g.load_cached(w + k);
+      rms8_stats<DT, VEC, HW>(p, a[c], g, st);
     }
   }
   float ss;
@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
     const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
     if (k >= p.K) continue;
     Pack<DT, VEC> g;
-    if (p.w) g.load_cached(w + k);
-    rms8_codes<DT, VEC>(p, a[c], g, inv, codes + k);
+    if (HW) g.load_cached(w + k);
+    rms8_codes<DT, VEC, HW, I8>(a[c], g, inv, codes + k);
   }
 }
 
@@ -343,7 +343,7 @@ struct RmsRing {
 };
 
 // Shared memory: slots x (x row, residual row), then the barriers.
-template <int DT, int CH>
+template <int DT, int CH, bool HW, bool I8>
 __global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const RmsRing g) {
   using E = typename ElemOf<DT>::type;
   constexpr int VEC = 16 / sizeof(E);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const
   uint32_t ph = 0;
   int it = 0;
   for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x, it ^= 1) {
-    if (p.w && row >= w_end) {
+    if (HW && row >= w_end) {
       const int64_t w_row = p.w_rows ? row / p.w_rows : 0;
       w_end = p.w_rows ? (w_row + 1) * p.w_rows : g.M;
       const E* src = static_cast<const E*>(p.w) + w_row * p.ldw;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const
           add_to(a[c], b);
         }
         if (p.h) a[c].store(static_cast<E*>(p.h) + row * p.ldh + k);
-        rms8_stats<DT, VEC>(p, a[c], w[c], st);
+        rms8_stats<DT, VEC, HW>(p, a[c], w[c], st);
       }
     }
     float ss;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const
   #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int k = (c * nt + static_cast<int>(threadIdx.x)) * VEC;
-      if (k < p.K) rms8_codes<DT, VEC>(p, a[c], w[c], inv, p.codes + row * p.ldc + k);
+      if (k < p.K) rms8_codes<DT, VEC, HW, I8>(a[c], w[c], inv, p.codes + row * p.ldc + k);
     }
     if (++slot == g.slots) { slot = 0; ph ^= 1; }
   }

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <type_traits>
 #include <utility>
 
 #include "host_common.cuh"
@@ -71,14 +72,25 @@ bool overlap(const Region& a, const Region& b) {
 bool same(const Region& a, const Region& b) { return a.p == b.p && (a.ld == b.ld || a.rows == 1); }
 
 // ------------------------------------------------------------------ RMS norm
-constexpr int kRmsSlots = 4;               // rows in flight per CTA of the ring form, at most (at least 2)
+constexpr int kRmsSlots = 2;               // rows of a CTA of the ring form
 constexpr int kRmsRingMax = 220 * 1024;    // its shared memory
+
+// call(has weight, INT8) as constants
+template <class F>
+svdq_status rms_kinds(const RmsParams& p, F call) {
+  using std::false_type;
+  using std::true_type;
+  if (p.w) return p.int8 ? call(true_type{}, true_type{}) : call(true_type{}, false_type{});
+  return p.int8 ? call(false_type{}, true_type{}) : call(false_type{}, false_type{});
+}
 
 template <int DT, int VEC, int CH>
 svdq_status launch_rms_t(const RmsParams& p, int64_t M, int nt, cudaStream_t st) {
   LaunchCfg lc(dim3(static_cast<unsigned>(M)), dim3(nt), 0, st);
-  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_kernel<DT, VEC, CH>, p));
-  return SVDQ_OK;
+  return rms_kinds(p, [&](auto hw, auto i8) -> svdq_status {
+    SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_kernel<DT, VEC, CH, hw.value, i8.value>, p));
+    return SVDQ_OK;
+  });
 }
 
 template <int DT, int VEC>
@@ -102,28 +114,34 @@ svdq_status launch_rms_v(const RmsParams& p, int64_t M, int sms, cudaStream_t st
 }
 
 // Many aligned rows (see rms8_ring_kernel).
-template <int DT, int CH>
-svdq_status launch_rms_ring_t(const RmsParams& p, int64_t M, int sms, int nt, cudaStream_t st) {
+template <int DT, int CH, bool HW, bool I8>
+svdq_status launch_rms_ring_k(const RmsParams& p, int64_t M, int sms, int nt, cudaStream_t st) {
   const int row_bytes = p.K * (DT == DT_FP32 ? 4 : 2);
   const int slot = row_bytes * (p.res ? 2 : 1);
-  if (svdq_status s = ensure_smem<rms8_ring_kernel<DT, CH>>(kRmsRingMax); s != SVDQ_OK) return s;
+  if (svdq_status s = ensure_smem<rms8_ring_kernel<DT, CH, HW, I8>>(kRmsRingMax); s != SVDQ_OK) return s;
   static std::atomic<int> known{0};  // registers per thread: the same on every device
   int regs = known.load(std::memory_order_relaxed);
   if (regs == 0) {
     cudaFuncAttributes fa;
-    SVDQ_TRY(cudaFuncGetAttributes(&fa, rms8_ring_kernel<DT, CH>));
+    SVDQ_TRY(cudaFuncGetAttributes(&fa, rms8_ring_kernel<DT, CH, HW, I8>));
     known.store(regs = std::max(16, fa.numRegs), std::memory_order_relaxed);
   }
-  // resident CTAs by registers (granted per warp in steps of 8 a thread),
-  // threads and two slots each; the shared memory that this leaves makes more slots
+  // as many persistent CTAs as are resident at once: by shared memory, by
+  // registers (granted per warp in steps of 8 a thread), by threads.  More
+  // slots a CTA instead of more CTAs was slower (16896 x 12288: 102 us with two
+  // slots, 109 with four)
+  const int smem = kRmsSlots * slot;
   const int by_regs = 65536 / (static_cast<int>(cdiv(regs, 8) * 8) * nt);
-  const int per_sm = std::max(1, std::min({(227 * 1024) / (2 * slot + 2048), by_regs, 2048 / nt, 32}));
-  const int slots = std::min({kRmsSlots, kRmsRingMax / slot, (227 * 1024 / per_sm - 2048) / slot});
-  RmsRing g{M, slots, row_bytes, kDefaultTimeoutNs};
-  const int smem = slots * slot;
+  const int per_sm = std::max(1, std::min({(227 * 1024) / (smem + 2048), by_regs, 2048 / nt, 32}));
+  RmsRing g{M, kRmsSlots, row_bytes, kDefaultTimeoutNs};
   LaunchCfg lc(dim3(static_cast<unsigned>(std::min<int64_t>(M, static_cast<int64_t>(sms) * per_sm))), dim3(nt), smem, st);
-  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_ring_kernel<DT, CH>, p, g));
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_ring_kernel<DT, CH, HW, I8>, p, g));
   return SVDQ_OK;
+}
+
+template <int DT, int CH>
+svdq_status launch_rms_ring_t(const RmsParams& p, int64_t M, int sms, int nt, cudaStream_t st) {
+  return rms_kinds(p, [&](auto hw, auto i8) { return launch_rms_ring_k<DT, CH, hw.value, i8.value>(p, M, sms, nt, st); });
 }
 
 template <int DT>
@@ -131,8 +149,11 @@ svdq_status launch_rms_ring(const RmsParams& p, int64_t M, int sms, cudaStream_t
   constexpr int V = DT == DT_FP32 ? 4 : 8;
   const int64_t pieces = p.K / V;
   auto threads = [&](int c) { return static_cast<int>(cdiv(cdiv(pieces, c), 32) * 32); };
-  // two pieces a thread for short rows and where an SM has few rows (latency), else four
-  if (threads(2) <= 128 || (M <= 4 * sms && threads(2) <= 512)) return launch_rms_ring_t<DT, 2>(p, M, sms, threads(2), st);
+  // 16-byte pieces a thread: one for short rows (16384 x 256: 8.0 us, 8.6 with
+  // two), two where an SM has few rows and latency counts, else four, which
+  // spread a row's fixed cost over fewer warps (4608 x 3072: 19.4 us, 20.2 with one)
+  if (threads(1) <= 128) return launch_rms_ring_t<DT, 1>(p, M, sms, threads(1), st);
+  if (M <= 4 * sms && threads(2) <= 512) return launch_rms_ring_t<DT, 2>(p, M, sms, threads(2), st);
   return launch_rms_ring_t<DT, 4>(p, M, sms, threads(4), st);
 }
 
@@ -144,7 +165,9 @@ svdq_status launch_rms(const RmsParams& p, int64_t M, int sms, cudaStream_t st) 
                    aligned(p.codes, V) && p.ldc % V == 0;
   if (!vec) return launch_rms_v<DT, 1>(p, M, sms, st);
   const int64_t slot = static_cast<int64_t>(p.K) * (DT == DT_FP32 ? 4 : 2) * (p.res ? 2 : 1);
-  if (M > sms && 2 * slot <= kRmsRingMax && p.K / V <= 4 * 512) return launch_rms_ring<DT>(p, M, sms, st);
+  // From more than one row an SM on, the ring (4608 x 3072 bf16 with residual:
+  // 19.4 us, 22.6 direct; 300 x 3072: 2.9, 3.8 direct; 148 x 3072: 2.4, 2.2 direct)
+  if (M > sms && kRmsSlots * slot <= kRmsRingMax && p.K / V <= 4 * 512) return launch_rms_ring<DT>(p, M, sms, st);
   return launch_rms_v<DT, V>(p, M, sms, st);
 }
 
