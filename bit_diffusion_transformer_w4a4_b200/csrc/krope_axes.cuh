@@ -11,10 +11,10 @@
 // Angles: an fp32 product of a far position and its frequency is off by whole
 // radians, so the angle is formed in fp64 and in half turns (the plan holds
 // f / pi), reduced by whole turns to [-1, 1], and only then goes through the
-// fp32 sincospi.  One CTA computes the angles of its few tokens once into
-// shared memory; every thread keeps the (cos, sin) of its own elements in
-// registers while it walks over the heads of Q and K, so the fp64 work is paid
-// per token and not per head.
+// fp32 sincospi.  A persistent CTA takes groups of a few tokens; the angles of
+// its next group are computed into shared memory under the first loads of the
+// present one, and every thread uses the (cos, sin) of its own elements for
+// all heads of Q and K, so the fp64 work is paid per token and not per head.
 //
 // Bound by memory: every element is read once and written once, in 16-byte
 // pieces where the layout allows (else one pair per thread).
@@ -27,7 +27,8 @@ namespace svdq {
 constexpr int ROPE_MAX_D = 256;
 constexpr int ROPE_MAX_PAIRS = ROPE_MAX_D / 2;
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_TOKENS = 4;   // tokens per CTA
+constexpr int ROPE_TOKENS = 4;   // tokens per group
+constexpr int ROPE_CTAS = 4;     // resident CTAs per SM
 
 struct RopePlan {
   double f[ROPE_MAX_PAIRS];      // half turns per unit of position
@@ -52,7 +53,7 @@ struct RopeParams {
   RopePlan plan;
   RopePos pos;
   RopeTensor t[2];
-  int64_t S, tokens;             // tokens per sequence and in all
+  uint32_t S, tokens, groups;    // tokens per sequence and in all, groups of ROPE_TOKENS
   float sign;                    // -1: inverse
   int pass;                      // elements beyond the rotated span are copied
 };
@@ -74,86 +75,118 @@ __device__ __forceinline__ float2 rope_cos_sin(const RopePos& pos, int64_t b, in
 // (VEC / 2 pairs), of the split form two pieces (VEC pairs); the scalar unit
 // is one pair in both.  Units beyond the rotating ones copy one piece.
 template <int DT, int VEC, bool INTER>
-__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_axes_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_axes_kernel(const __grid_constant__ RopeParams p) {
   using E = typename ElemOf<DT>::type;
   constexpr bool TWO = !INTER || VEC == 1;                   // a unit's pairs span two pieces
   constexpr int NP = TWO ? VEC : VEC / 2;                    // pairs per rotating unit
   constexpr int HB = TWO ? 2 : 4;
-  __shared__ float2 cs[ROPE_TOKENS][ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float cosines[2][ROPE_TOKENS][ROPE_MAX_PAIRS], sines[2][ROPE_TOKENS][ROPE_MAX_PAIRS];
   __shared__ double freq[ROPE_MAX_PAIRS];
   __shared__ uint8_t axis[ROPE_MAX_PAIRS];
-  if (threadIdx.x < p.plan.pairs) {  // lanes' own indexes into the parameters replay: once per pair, not per angle
+  const int pairs = p.plan.pairs;
+  if (threadIdx.x < pairs) {  // lanes' own indexes into the parameters replay: once per CTA, not per angle
     freq[threadIdx.x] = p.plan.f[threadIdx.x];
     axis[threadIdx.x] = p.plan.axis[threadIdx.x];
   }
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const int pairs = p.plan.pairs;
-  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * ROPE_TOKENS;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(ROPE_TOKENS), p.tokens - tok0));
-  for (int i = threadIdx.x; i < nt * pairs; i += ROPE_THREADS) {
-    const int t = i / pairs, pr = i - t * pairs;
-    const int64_t tok = tok0 + t;
-    float2 v = rope_cos_sin(p.pos, tok / p.S, tok % p.S, axis[pr], freq[pr]);
-    v.y *= p.sign;
-    cs[t][pr] = v;
-  }
-  __syncthreads();
+  auto tokens_of = [&](uint32_t group) {
+    const uint32_t first = group * ROPE_TOKENS;
+    return first < p.tokens ? static_cast<int>(min(static_cast<uint32_t>(ROPE_TOKENS), p.tokens - first)) : 0;
+  };
+  auto angles = [&](uint32_t group, int buf) {
+    const int n = tokens_of(group);
+    for (int i = threadIdx.x; i < n * pairs; i += ROPE_THREADS) {
+      const int t = i / pairs, pr = i - t * pairs;
+      const uint32_t tok = group * ROPE_TOKENS + t, b = tok / p.S;
+      const float2 v = rope_cos_sin(p.pos, b, tok - b * p.S, axis[pr], freq[pr]);
+      cosines[buf][t][pr] = v.x;
+      sines[buf][t][pr] = v.y * p.sign;
+    }
+  };
 
   const int rot = pairs / NP;                                // rotating units
   const int units = rot + (p.pass ? (p.plan.D - 2 * pairs) / VEC : 0);
   const int lanes = ROPE_THREADS / units;
   const int u = threadIdx.x % units;
-  const int lane = threadIdx.x / units;
-  if (lane >= lanes) return;
-  // lanes share out the tokens first, then the heads of a token
-  const int per = max(1, lanes / nt);                        // head lanes per token
-  const int H0 = p.t[0].heads, heads = H0 + p.t[1].heads;
+  const int lane = threadIdx.x / units;                      // >= lanes: helps with the angles only
   const bool turns = u < rot;
   const int step = INTER ? 1 : pairs;                        // from a pair's first element to its second
   const int off = !turns ? 2 * pairs + (u - rot) * VEC : INTER ? u * NP * 2 : u * NP;
-  for (int t = lane / per; t < nt; t += max(1, lanes / per)) {
-    const int64_t tok = tok0 + t, b = tok / p.S, s = tok % p.S;
-    const E* x0 = static_cast<const E*>(p.t[0].x) + b * p.t[0].xb + s * p.t[0].xs + off;
-    const E* x1 = static_cast<const E*>(p.t[1].x) + b * p.t[1].xb + s * p.t[1].xs + off;
-    E* o0 = static_cast<E*>(p.t[0].out) + b * p.t[0].ob + s * p.t[0].os + off;
-    E* o1 = static_cast<E*>(p.t[1].out) + b * p.t[1].ob + s * p.t[1].os + off;
-    float2 c[NP];
+
+  int buf = 0;
+  angles(blockIdx.x, 0);
+  __syncthreads();
+  for (uint32_t group = blockIdx.x; group < p.groups; group += gridDim.x, buf ^= 1) {
+    const int nt = tokens_of(group);
+    // lanes share out the tokens first, then the heads of a token
+    const int per = max(1, lanes / nt);                      // head lanes per token
+    bool ahead = true;                                       // the next group's angles are still to do
+    for (int t = lane < lanes ? lane / per : nt; t < nt; t += max(1, lanes / per)) {
+      const uint32_t tok = group * ROPE_TOKENS + t, b = tok / p.S, s = tok - b * p.S;
+      const int h0 = lane % per;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {                          // Q, K
+        const RopeTensor& q = p.t[w];
+        const E* x = static_cast<const E*>(q.x) + b * q.xb + s * q.xs + h0 * q.xh + off;
+        E* o = static_cast<E*>(q.out) + b * q.ob + s * q.os + h0 * q.oh + off;
+        const int64_t dx = per * q.xh, dy = per * q.oh;
+#pragma unroll 1
+        for (int left = q.heads - h0; left > 0; left -= per * HB) {
+          // HB heads' loads go out before the first is used
+          Pack<DT, VEC> va[HB], vb[TWO ? HB : 1];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) c[i] = turns ? cs[t][u * NP + i] : make_float2(1.f, 0.f);
-    for (int h0 = lane % per; h0 < heads; h0 += per * HB) {
-      // HB heads' loads go out before the first is used
-      Pack<DT, VEC> va[HB], vb[TWO ? HB : 1];
-#pragma unroll
-      for (int j = 0; j < HB; ++j) {
-        const int hh = h0 + j * per;
-        if (hh < heads) {
-          const E* x = hh < H0 ? x0 + hh * p.t[0].xh : x1 + (hh - H0) * p.t[1].xh;
-          va[j].load(x);
-          if (TWO && turns) vb[TWO ? j : 0].load(x + step);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < HB; ++j) {
-        const int hh = h0 + j * per;
-        if (hh < heads) {
-          E* o = hh < H0 ? o0 + hh * p.t[0].oh : o1 + (hh - H0) * p.t[1].oh;
-          if (turns) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              E& ea = TWO ? va[j].e[i] : va[j].e[(2 * i) % VEC];
-              E& eb = TWO ? vb[TWO ? j : 0].e[i] : va[j].e[(2 * i + 1) % VEC];
-              const float a0 = to_f32<DT>(ea), b0 = to_f32<DT>(eb);
-              ea = from_f32<DT>(a0 * c[i].x - b0 * c[i].y);
-              eb = from_f32<DT>(a0 * c[i].y + b0 * c[i].x);
+          for (int j = 0; j < HB; ++j) {
+            if (j * per < left) {
+              va[j].load(x);
+              if (TWO && turns) vb[TWO ? j : 0].load(x + step);
             }
-            if (TWO) vb[TWO ? j : 0].store(o + step);
+            x += dx;
           }
-          va[j].store(o);
+          if (ahead) {  // under the first loads
+            ahead = false;
+            angles(group + gridDim.x, buf ^ 1);
+          }
+          const float* c = &cosines[buf][t][u * NP];
+          const float* sn = &sines[buf][t][u * NP];
+#pragma unroll
+          for (int j = 0; j < HB; ++j) {
+            if (j * per < left) {
+              if (turns) {
+                if constexpr (VEC == 1) {
+                  const float a0 = to_f32<DT>(va[j].e[0]), b0 = to_f32<DT>(vb[j].e[0]);
+                  va[j].e[0] = from_f32<DT>(a0 * c[0] - b0 * sn[0]);
+                  vb[j].e[0] = from_f32<DT>(a0 * sn[0] + b0 * c[0]);
+                } else if constexpr (INTER) {
+#pragma unroll
+                  for (int i = 0; i < NP; ++i) {
+                    const uint64_t v = get2(va[j], i);
+                    const float a0 = f2_lo(v), b0 = f2_hi(v);
+                    set2(va[j], i, f2_pack(a0 * c[i] - b0 * sn[i], a0 * sn[i] + b0 * c[i]));
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < NP / 2; ++i) {         // two pairs at a time
+                    const uint64_t a2 = get2(va[j], i), b2 = get2(vb[j], i);
+                    const uint64_t c2 = *reinterpret_cast<const uint64_t*>(c + 2 * i);
+                    const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sn + 2 * i);
+                    const uint64_t n2 = s2 ^ 0x8000000080000000ull;
+                    set2(va[j], i, f2_fma(b2, n2, f2_mul(a2, c2)));
+                    set2(vb[j], i, f2_fma(b2, c2, f2_mul(a2, s2)));
+                  }
+                }
+                if (TWO) vb[TWO ? j : 0].store(o + step);
+              }
+              va[j].store(o);
+            }
+            o += dy;
+          }
         }
       }
     }
+    if (ahead) angles(group + gridDim.x, buf ^ 1);
+    __syncthreads();
   }
 }
 

@@ -173,22 +173,23 @@ svdq_status launch_rms(const RmsParams& p, int64_t M, int sms, cudaStream_t st) 
 
 // --------------------------------------------------------------------- rotary
 template <int DT, int VEC>
-svdq_status launch_rope_v(const RopeParams& p, cudaStream_t st) {
-  LaunchCfg lc(dim3(static_cast<unsigned>(cdiv(p.tokens, ROPE_TOKENS))), dim3(ROPE_THREADS), 0, st);
+svdq_status launch_rope_v(const RopeParams& p, int sms, cudaStream_t st) {
+  LaunchCfg lc(dim3(static_cast<unsigned>(std::min<int64_t>(p.groups, static_cast<int64_t>(sms) * ROPE_CTAS))),
+               dim3(ROPE_THREADS), 0, st);
   SVDQ_TRY(p.plan.interleaved ? cudaLaunchKernelEx(&lc.cfg, rope_axes_kernel<DT, VEC, true>, p)
                               : cudaLaunchKernelEx(&lc.cfg, rope_axes_kernel<DT, VEC, false>, p));
   return SVDQ_OK;
 }
 
 template <int DT>
-svdq_status launch_rope(const RopeParams& p, cudaStream_t st) {
+svdq_status launch_rope(const RopeParams& p, int sms, cudaStream_t st) {
   constexpr int V = DT == DT_FP32 ? 4 : 8;
   const int R = 2 * p.plan.pairs;
   bool vec = (p.plan.interleaved ? R : R / 2) % V == 0 && (p.plan.D - R) % V == 0;
   for (const RopeTensor& t : p.t)
     vec = vec && (t.heads == 0 || (aligned16(t.x) && aligned16(t.out) && t.xb % V == 0 && t.xs % V == 0 &&
                                    t.xh % V == 0 && t.ob % V == 0 && t.os % V == 0 && t.oh % V == 0));
-  return vec ? launch_rope_v<DT, V>(p, st) : launch_rope_v<DT, 1>(p, st);
+  return vec ? launch_rope_v<DT, V>(p, sms, st) : launch_rope_v<DT, 1>(p, sms, st);
 }
 
 svdq_status rope_pos(const svdq_rope_positions* pos, RopePos* out) {
@@ -543,13 +544,14 @@ svdq_status svdq_rope_apply(svdq_rope_t h, svdq_dtype dtype, int64_t B, int64_t 
   DeviceInfo dev;
   if (svdq_status s = device_info(&dev); s != SVDQ_OK) return s;
   p.plan = h->plan;
-  p.S = S;
-  p.tokens = B * S;
+  p.S = static_cast<uint32_t>(S);
+  p.tokens = static_cast<uint32_t>(B * S);
+  p.groups = static_cast<uint32_t>(cdiv(B * S, ROPE_TOKENS));
   p.sign = inverse ? -1.f : 1.f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == SVDQ_BF16) return launch_rope<DT_BF16>(p, st);
-  if (dtype == SVDQ_FP16) return launch_rope<DT_FP16>(p, st);
-  return launch_rope<DT_FP32>(p, st);
+  if (dtype == SVDQ_BF16) return launch_rope<DT_BF16>(p, dev.sms, st);
+  if (dtype == SVDQ_FP16) return launch_rope<DT_FP16>(p, dev.sms, st);
+  return launch_rope<DT_FP32>(p, dev.sms, st);
 }
 
 svdq_status svdq_rope_table(svdq_rope_t h, int64_t B, int64_t S, const svdq_rope_positions* pos, float* table,
