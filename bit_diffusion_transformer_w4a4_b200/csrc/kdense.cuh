@@ -27,6 +27,11 @@ namespace svdq {
 
 enum : int { DK_F16 = 0, DK_E4M3 = 1, DK_INT8 = 2 };       // operand kinds
 enum : int { DENSE_NONE = 0, DENSE_GELU = 1, DENSE_SILU = 2 };
+// How Y is stored and the residual loaded, by their alignment: 2 bytes at a
+// time (any), 4 bytes after an exchange between lanes (N and the row distances
+// even), or as tiles through shared memory and tensor maps (16-byte aligned
+// rows; pair kernel only).
+enum : int { STORE_PLAIN = 0, STORE_PAIRED = 1, STORE_TILED = 2 };
 
 struct DenseParams {
   uint16_t* y;
@@ -41,7 +46,7 @@ struct DenseParams {
   int kblk;               // 128-byte k-blocks
   int num_f, num_t;       // feature and token tiles
   int act;
-  int paired;             // stores and residual loads of two features (see dense_store)
+  int store;              // form of the stores and residual loads (below)
   int* err;               // or null
   uint64_t timeout_ns;
 };
@@ -169,7 +174,6 @@ __device__ __forceinline__ void dense_math(const DenseParams& p, DenseLane& l, i
 
 // Stores.  In the plain form a lane owns its feature's column of Y: 2 bytes a
 // store, 64 contiguous bytes a warp, any alignment.  In the paired form
-// (p.paired: N and the row distances even, Y and the residual 4-byte aligned)
 // lanes 2i and 2i + 1 first exchange values, so that the even lane holds both
 // features for token j and the odd one both for token j + 1: half the loads
 // and stores, and half the registers of a prefetched residual.
@@ -240,21 +244,27 @@ __device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLan
 // its 128 features x BN tokens.  Persistent over tiles; two accumulators in
 // tensor memory, so the epilogue of one tile runs under the MMAs of the next.
 // Warps: 0 TMA, 1 MMA and tensor memory, 2-3 idle, 4-19 epilogue: each of the
-// 16 takes 32 features x BN / 4 tokens.  Their loads for a tile (scales,
-// residual) go out before they wait for its accumulator.
+// 16 takes 32 features x 64 tokens.  In the tiled form a warp has a 4 KB box of
+// its own in shared memory: the residual arrives in it by a tensor load while
+// the tile is being summed, the accumulator is read in the matrix-fragment
+// layout, stmatrix transposes the rounded result into the box in place, and a
+// tensor store takes it from there.  That is an eighth of an instruction per
+// element where lane exchanges and 4-byte stores take about five, and under
+// the power limit that these calls run into, instructions are clock rate.
 constexpr int DP_THREADS = 640;
 constexpr int DP_EPI_WARPS = 16;
 
-template <int BN>
 struct DensePairSmem {
+  static constexpr int BN = 256;
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int A_BYTES = BN / 2 * 128;
   static constexpr int STAGE = W_BYTES + A_BYTES;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int STAGES = 5;
   static constexpr uint32_t TX = 2 * STAGE;
-  static constexpr int BAR_OFF = STAGES * STAGE;
-  static constexpr int SA_OFF = BAR_OFF + 256;              // [16 warps][BN / 4] token scales
-  static constexpr int TOTAL = SA_OFF + DP_EPI_WARPS * BN + 1024;
+  static constexpr int OUT_OFF = STAGES * STAGE;            // [16 warps][64 tokens][32 features], 64-byte swizzle
+  static constexpr int OUT_BYTES = 64 * 32 * 2;
+  static constexpr int BAR_OFF = OUT_OFF + DP_EPI_WARPS * OUT_BYTES;
+  static constexpr int TOTAL = BAR_OFF + 512 + 1024;
   static_assert(TOTAL <= 232448, "shared memory per CTA");
 };
 
@@ -269,11 +279,102 @@ __device__ __forceinline__ void dense_tile(const DenseParams& p, int tile, int& 
   tt = band * kDenseBand + in - ft * wide;
 }
 
-template <int KIND, int OUT, int BN>
+// The tiled epilogue of one warp: 32 features from n0, 64 tokens from m0.
+// box: its shared memory, holding the residual if there is one.
+template <int KIND, int OUT>
+__device__ __forceinline__ void dense_tile_out(const DenseParams& p, uint32_t taddr, uint32_t box, int n0, int m0, int lane) {
+  const int fr = lane >> 2, tc = 2 * (lane & 3);  // fragment row (feature) and column (token)
+  uint64_t sa[8];
+  if (KIND != DK_F16 && p.sa) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int m = m0 + 8 * k + tc;
+      sa[k] = f2_pack(m < p.M ? __ldg(p.sa + m) : 0.f, m + 1 < p.M ? __ldg(p.sa + m + 1) : 0.f);
+    }
+  }
+  const int g0 = p.gate ? m0 / p.gate_rows : 0;
+  const bool one_gate = p.gate && (min(m0 + 64, p.M) <= (g0 + 1) * p.gate_rows);
+  // lane 8 i + j: token j of column block (i / 2), feature block i % 2
+  const int mtok = ((lane >> 4) << 3) + (lane & 7), mfeat = (lane >> 3) & 1;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    uint32_t v[32];
+    tmem_ld_16x256b_x8(taddr + (static_cast<uint32_t>(16 * half) << 16), v);
+    const int na = n0 + 16 * half + fr, nb = na + 8;
+    float bias[2] = {0.f, 0.f}, sw[2] = {1.f, 1.f}, gate[2] = {0.f, 0.f};
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int n = f ? nb : na;
+      if (n < p.N) {
+        if (p.bias) bias[f] = to_f32<OUT>(__ldg(p.bias + n));
+        if (KIND != DK_F16 && p.sw) sw[f] = __ldg(p.sw + n);
+        if (one_gate) gate[f] = to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>(g0) * p.ldg + n));
+      }
+    }
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      uint64_t x[4];  // (block k, feature a), (k, b), (k + 1, a), (k + 1, b): a pair of tokens each
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = v[4 * (k + i / 2) + 2 * (i % 2)], hi = v[4 * (k + i / 2) + 2 * (i % 2) + 1];
+        x[i] = KIND == DK_INT8 ? f2_pack(static_cast<float>(static_cast<int>(lo)), static_cast<float>(static_cast<int>(hi)))
+                               : f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+        const uint64_t b2 = f2_pack(bias[i % 2], bias[i % 2]);
+        if constexpr (KIND != DK_F16) {
+          if (p.sa) x[i] = f2_mul(x[i], sa[k + i / 2]);
+          x[i] = f2_fma(x[i], f2_pack(sw[i % 2], sw[i % 2]), b2);
+        } else {
+          x[i] = f2_add(x[i], b2);
+        }
+      }
+      if (p.act == DENSE_GELU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = gelu_tanh2(x[i]);
+      } else if (p.act == DENSE_SILU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = silu2(x[i]);
+      }
+      if (p.gate) {
+        if (one_gate) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], f2_pack(gate[i % 2], gate[i % 2]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = i % 2 ? nb : na, m = m0 + 8 * (k + i / 2) + tc;
+            float g[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              g[j] = n < p.N && m + j < p.M
+                         ? to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>((m + j) / p.gate_rows) * p.ldg + n)) : 0.f;
+            x[i] = f2_mul(x[i], f2_pack(g[0], g[1]));
+          }
+        }
+      }
+      const uint32_t at = box + swz_off(8 * k + mtok, 2 * half + mfeat, 64);
+      if (p.res) {
+        uint32_t r[4];
+        ldmatrix_x4_trans(at, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = f2_add(x[i], f2_pack(to_f32<OUT>(static_cast<uint16_t>(r[i])), to_f32<OUT>(static_cast<uint16_t>(r[i] >> 16))));
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = pack_out<OUT>(f2_lo(x[i]), f2_hi(x[i]));
+      stmatrix_x4_trans(at, o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+template <int KIND, int OUT>
 __global__ void __launch_bounds__(DP_THREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                      const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
                       const __grid_constant__ DenseParams p) {
-  using S = DensePairSmem<BN>;
+  using S = DensePairSmem;
+  constexpr int BN = S::BN;
   constexpr int NST = S::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -285,6 +386,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
   const uint32_t bar_acc_empty = smem_u32(bars + 2 * NST + 2);  // two, the leader's count
   const uint32_t bar_drain = smem_u32(bars + 2 * NST + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 5);
+  const uint32_t bar_res = smem_u32(bars + 2 * NST + 6);        // one per epilogue warp
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -305,6 +407,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
       mbar_init(bar_acc_empty + 8 * i, 2 * DP_EPI_WARPS);
     }
     mbar_init(bar_drain, 1);
+    for (int i = 0; i < DP_EPI_WARPS; ++i) mbar_init(bar_res + 8 * i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -387,27 +490,62 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     const int q = warp & 3;              // tensor-memory lane group of this warp
     const int c0 = (e >> 2) * CW;
     const uint32_t acc_empty0 = mapa_shared(bar_acc_empty, 0);
-    float* sa = reinterpret_cast<float*>(smem + S::SA_OFF) + e * CW;
+    const uint32_t box = sbase + S::OUT_OFF + e * S::OUT_BYTES;
+    const uint32_t res_full = bar_res + 8 * e;
+    uint32_t res_ph = 0;
+    bool res_on = false;                 // a residual load is in flight
     for (int tile = cid, j = 0; tile < num_tiles; tile += nclu, ++j) {
       int ft, tt;
       dense_tile(p, tile, ft, tt);
       const int ac = j & 1;
-      const int n = ft * 256 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int n0 = ft * 256 + static_cast<int>(rank) * 128 + q * 32;
       const int m0 = tt * BN + c0;
-      DenseLane l = dense_lane<OUT>(p, n, m0);
-      if (KIND != DK_F16 && p.sa) {
-        __syncwarp();  // the previous tile's scales have been read
-        for (int i = lane; i < CW; i += 32) sa[i] = m0 + i < p.M ? __ldg(p.sa + m0 + i) : 0.f;
-        __syncwarp();
-      }
-      const float* sc = KIND != DK_F16 && p.sa ? sa : nullptr;
       const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + ac * 256 + c0;
       auto acc_read = [&] {  // this warp has read its part of the accumulator
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * ac);
       };
-      if (p.paired) {
+      if (p.store == STORE_TILED) {
+        const bool on = n0 < p.N && m0 < p.M;
+        if (lane == 0) bulk_wait_read();  // the previous tile has left the box
+        if (p.res && on && lane == 0) {
+          mbar_expect_tx(res_full, S::OUT_BYTES);
+          tma_load_2d(box, &tm_r, res_full, n0, m0);
+        }
+        res_on = p.res && on;
+        if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
+        tc_fence_after();
+        if (on) {
+          if (p.res) {
+            if (!__all_sync(0xffffffffu, wait_bounded(res_full, res_ph, guard, 0x305))) break;
+            res_ph ^= 1;
+            res_on = false;
+          }
+          dense_tile_out<KIND, OUT>(p, ta, box, n0, m0, lane);
+        }
+        acc_read();
+        if (on) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_y, box, n0, m0);
+            bulk_commit();
+          }
+        }
+        continue;
+      }
+      const int n = n0 + lane;
+      DenseLane l = dense_lane<OUT>(p, n, m0);
+      // the box holds this warp's token scales
+      float* sa = reinterpret_cast<float*>(smem + S::OUT_OFF + e * S::OUT_BYTES);
+      if (KIND != DK_F16 && p.sa) {
+        __syncwarp();  // the previous tile's scales have been read
+        for (int i = lane; i < CW; i += 32) sa[i] = m0 + i < p.M ? __ldg(p.sa + m0 + i) : 0.f;
+        __syncwarp();
+      }
+      const float* sc = KIND != DK_F16 && p.sa ? sa : nullptr;
+      if (p.store == STORE_PAIRED) {
         uint32_t r[CW / 2];
         if (p.res) dense_residual<OUT, CW, true>(p, l, m0, n, r);
         if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
@@ -437,6 +575,14 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
           dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
         }
       }
+    }
+    if (lane == 0) {
+      if (res_on) {  // given up with the residual on its way
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(res_full, res_ph) && global_timer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+      bulk_wait_all();  // the stores are done before the shared memory goes
     }
   }
 
@@ -595,12 +741,12 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
           uint64_t x[8];
           tmem_ld_x16(ta + c, v);
           if (p.res) {
-            if (p.paired) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
+            if (p.store >= STORE_PAIRED) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
             else dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
           }
           tmem_ld_wait();
           dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
-          if (p.paired) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
+          if (p.store >= STORE_PAIRED) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
           else dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
         }
       }

@@ -251,16 +251,16 @@ constexpr int64_t kRopeMaxSpan = 1ll << 44;  // elements of a dimension's extent
 // ---------------------------------------------------------------------- dense
 // Clusters of two CTAs that fit on the device at once (cached per device,
 // stored + 1).
-template <int KIND, int OUT, int BN>
+template <int KIND, int OUT>
 int dense_pair_clusters(const DeviceInfo& d) {
   static std::atomic<int> cache[64];
   if (d.dev < 0 || d.dev >= 64) return 0;
   if (const int known = cache[d.dev].load(std::memory_order_acquire); known > 0) return known - 1;
-  constexpr int smem = DensePairSmem<BN>::TOTAL;
-  if (ensure_smem<dense_pair_kernel<KIND, OUT, BN>>(smem) != SVDQ_OK) return 0;
+  constexpr int smem = DensePairSmem::TOTAL;
+  if (ensure_smem<dense_pair_kernel<KIND, OUT>>(smem) != SVDQ_OK) return 0;
   LaunchCfg lc(dim3(2 * (d.sms / 2)), dim3(DP_THREADS), smem, nullptr, 2);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, OUT, BN>, &lc.cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, OUT>, &lc.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;  // not cached: the next call asks again
   }
@@ -274,6 +274,7 @@ struct DenseCall {
   DenseParams p;
   cudaStream_t st;
   int64_t lda, ldw;  // bytes
+  bool tiled;        // Y and the residual can go through tensor maps
 };
 
 // Maps of W and A with boxes of 128 bytes x rows.
@@ -289,18 +290,31 @@ svdq_status dense_maps(const DenseCall& c, int wrows, int arows, CUtensorMap* tw
   return make_tmap(ta, c.d->a, dt, es, c.d->K, c.d->M, 128 / es, arows, CU_TENSOR_MAP_SWIZZLE_128B, c.lda);
 }
 
-template <int KIND, int OUT, int BN>
+template <int KIND, int OUT>
 svdq_status launch_dense_pair(DenseCall& c) {
-  constexpr int smem = DensePairSmem<BN>::TOTAL;
-  const int clusters = dense_pair_clusters<KIND, OUT, BN>(c.dev);
+  constexpr int BN = DensePairSmem::BN;
+  constexpr int smem = DensePairSmem::TOTAL;
+  const int clusters = dense_pair_clusters<KIND, OUT>(c.dev);
   if (clusters < 1) return SVDQ_ERR_CUDA;
-  CUtensorMap tw, ta;
+  CUtensorMap tw, ta, ty, tr;
   if (svdq_status s = dense_maps<KIND, OUT>(c, 128, BN / 2, &tw, &ta); s != SVDQ_OK) return s;
+  ty = tr = ta;  // not used unless the stores are tiled
+  if (c.tiled) {
+    c.p.store = STORE_TILED;
+    constexpr CUtensorMapDataType dt = OUT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (svdq_status s = make_tmap(&ty, c.d->y, dt, 2, c.d->N, c.d->M, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B, 2 * c.d->ldy);
+        s != SVDQ_OK)
+      return s;
+    if (c.d->residual)
+      if (svdq_status s = make_tmap(&tr, c.d->residual, dt, 2, c.d->N, c.d->M, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B, 2 * c.d->ldr);
+          s != SVDQ_OK)
+        return s;
+  }
   c.p.num_f = static_cast<int>(cdiv(c.p.N, 256));
   c.p.num_t = static_cast<int>(cdiv(c.p.M, BN));
   const int tiles = c.p.num_f * c.p.num_t;
   LaunchCfg lc(dim3(2 * std::min(tiles, clusters)), dim3(DP_THREADS), smem, c.st, 2);
-  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_pair_kernel<KIND, OUT, BN>, tw, ta, c.p));
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_pair_kernel<KIND, OUT>, tw, ta, ty, tr, c.p));
   return SVDQ_OK;
 }
 
@@ -328,7 +342,6 @@ DenseChoice dense_choose(int64_t M, int64_t N, int kblk, int sms) {
   const int64_t nf = cdiv(N, 128);
   DenseChoice c{0, 16, 1};
   if (cdiv(N, 256) * cdiv(M, 256) >= sms / 2) return DenseChoice{1, 256, 1};
-  if (cdiv(N, 256) * cdiv(M, 128) >= sms / 2) return DenseChoice{1, 128, 1};
   while (c.bn < 128 && c.bn < M) c.bn *= 2;
   while (c.bn > 16 && nf * cdiv(M, c.bn) < sms / 2) c.bn /= 2;
   while (c.split < 8 && nf * cdiv(M, c.bn) * c.split * 2 <= 2 * sms && kblk >= 4 * c.split) c.split *= 2;
@@ -338,7 +351,7 @@ DenseChoice dense_choose(int64_t M, int64_t N, int kblk, int sms) {
 template <int KIND, int OUT>
 svdq_status launch_dense(DenseCall& c) {
   const DenseChoice v = dense_choose(c.p.M, c.p.N, c.p.kblk, c.dev.sms);
-  if (v.pair) return v.bn == 256 ? launch_dense_pair<KIND, OUT, 256>(c) : launch_dense_pair<KIND, OUT, 128>(c);
+  if (v.pair) return launch_dense_pair<KIND, OUT>(c);
   switch (v.bn) {
     case 16: return launch_dense_solo<KIND, OUT, 16>(c, v.split);
     case 32: return launch_dense_solo<KIND, OUT, 32>(c, v.split);
@@ -406,8 +419,12 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
   c.p.N = static_cast<int>(N);
   c.p.kblk = static_cast<int>(cdiv(K * es, 128));
   c.p.act = static_cast<int>(d->act);
-  c.p.paired = N % 2 == 0 && aligned(d->y, 4) && (M == 1 || d->ldy % 2 == 0) &&
-               (!d->residual || (aligned(d->residual, 4) && (M == 1 || d->ldr % 2 == 0)));
+  auto rows_by = [&](int64_t n) {  // Y's and the residual's rows start on multiples of n elements
+    return aligned(d->y, 2 * n) && (M == 1 || d->ldy % n == 0) &&
+           (!d->residual || (aligned(d->residual, 2 * n) && (M == 1 || d->ldr % n == 0)));
+  };
+  c.p.store = N % 2 == 0 && rows_by(2) ? STORE_PAIRED : STORE_PLAIN;
+  c.tiled = M > 1 && rows_by(8) && (!d->residual || d->ldr > 0);
   c.p.err = d->device_error;
   c.p.timeout_ns = kDefaultTimeoutNs;
   const bool bf = d->out == SVDQ_BF16;
