@@ -31,7 +31,7 @@ enum : int { DENSE_NONE = 0, DENSE_GELU = 1, DENSE_SILU = 2 };
 // time (any), 4 bytes after an exchange between lanes (N and the row distances
 // even), or as tiles through shared memory and tensor maps (16-byte aligned
 // rows; pair kernel only).
-enum : int { STORE_PLAIN = 0, STORE_PAIRED = 1, STORE_TILED = 2 };
+enum : int { STORE_PLAIN = 0, STORE_PAIRED = 1 };  // the tiled form is a kernel of its own
 
 struct DenseParams {
   uint16_t* y;
@@ -280,95 +280,109 @@ __device__ __forceinline__ void dense_tile(const DenseParams& p, int tile, int& 
 }
 
 // The tiled epilogue of one warp: 32 features from n0, 64 tokens from m0.
-// box: its shared memory, holding the residual if there is one.
+// Thread t works on features n0 + t / 4 + 8 f (f = 0 .. 3) and tokens
+// m0 + 8 k + 2 (t % 4) and + 1 (k = 0 .. 7).
 template <int KIND, int OUT>
-__device__ __forceinline__ void dense_tile_out(const DenseParams& p, uint32_t taddr, uint32_t box, int n0, int m0, int lane) {
-  const int fr = lane >> 2, tc = 2 * (lane & 3);  // fragment row (feature) and column (token)
-  uint64_t sa[8];
-  if (KIND != DK_F16 && p.sa) {
+struct DenseTileOut {
+  float bias[4], sw[4], gate[4];
+  uint64_t sa[8];  // scales of its token pairs
+  bool one_gate;   // all its tokens share a gate row (else the row is looked up per element)
+
+  // What does not depend on the accumulator, loaded while it is being summed.
+  __device__ __forceinline__ void prepare(const DenseParams& p, int n0, int m0, int lane) {
+    const int g0 = p.gate ? m0 / p.gate_rows : 0;
+    one_gate = p.gate && min(m0 + 64, p.M) <= (g0 + 1) * p.gate_rows;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int m = m0 + 8 * k + tc;
-      sa[k] = f2_pack(m < p.M ? __ldg(p.sa + m) : 0.f, m + 1 < p.M ? __ldg(p.sa + m + 1) : 0.f);
+    for (int f = 0; f < 4; ++f) {
+      const int n = n0 + 8 * f + (lane >> 2);
+      const bool on = n < p.N;
+      bias[f] = on && p.bias ? to_f32<OUT>(__ldg(p.bias + n)) : 0.f;
+      sw[f] = KIND != DK_F16 && on && p.sw ? __ldg(p.sw + n) : 1.f;
+      gate[f] = on && one_gate ? to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>(g0) * p.ldg + n)) : 0.f;
+    }
+    if (KIND != DK_F16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int m = m0 + 8 * k + 2 * (lane & 3);
+        sa[k] = p.sa ? f2_pack(m < p.M ? __ldg(p.sa + m) : 0.f, m + 1 < p.M ? __ldg(p.sa + m + 1) : 0.f) : f2_pack(1.f, 1.f);
+      }
     }
   }
-  const int g0 = p.gate ? m0 / p.gate_rows : 0;
-  const bool one_gate = p.gate && (min(m0 + 64, p.M) <= (g0 + 1) * p.gate_rows);
-  // lane 8 i + j: token j of column block (i / 2), feature block i % 2
-  const int mtok = ((lane >> 4) << 3) + (lane & 7), mfeat = (lane >> 3) & 1;
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    uint32_t v[32];
-    tmem_ld_16x256b_x8(taddr + (static_cast<uint32_t>(16 * half) << 16), v);
-    const int na = n0 + 16 * half + fr, nb = na + 8;
-    float bias[2] = {0.f, 0.f}, sw[2] = {1.f, 1.f}, gate[2] = {0.f, 0.f};
+
+  // box: the warp's shared memory, holding the residual if there is one.
+  // `done` is called when the accumulator has been read.
+  template <class F>
+  __device__ __forceinline__ void run(const DenseParams& p, uint32_t taddr, uint32_t box, int n0, int m0, int lane, F done) const {
+    // lane 8 i + j of a matrix access: token j of column block i / 2, feature block i % 2
+    const int mtok = ((lane >> 4) << 3) + (lane & 7), mfeat = (lane >> 3) & 1;
+    uint32_t v[2][16];
+    tmem_ld_16x256b_x4(taddr, v[0]);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int n = f ? nb : na;
-      if (n < p.N) {
-        if (p.bias) bias[f] = to_f32<OUT>(__ldg(p.bias + n));
-        if (KIND != DK_F16 && p.sw) sw[f] = __ldg(p.sw + n);
-        if (one_gate) gate[f] = to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>(g0) * p.ldg + n));
-      }
-    }
-    tmem_ld_wait();
+    for (int c = 0; c < 4; ++c) {  // 16 features x 32 tokens; the next chunk is read under this one
+      const int half = c / 2;
+      tmem_ld_wait();
+      if (c < 3)
+        tmem_ld_16x256b_x4(taddr + (static_cast<uint32_t>(16 * ((c + 1) / 2)) << 16) + 32 * ((c + 1) % 2), v[(c + 1) % 2]);
+      else
+        done();
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      uint64_t x[4];  // (block k, feature a), (k, b), (k + 1, a), (k + 1, b): a pair of tokens each
+      for (int kk = 0; kk < 4; kk += 2) {
+        const int k0 = 4 * (c % 2) + kk;
+        uint64_t x[4];  // (block k0, feature a), (k0, b), (k0 + 1, a), (k0 + 1, b): a pair of tokens each
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = v[4 * (k + i / 2) + 2 * (i % 2)], hi = v[4 * (k + i / 2) + 2 * (i % 2) + 1];
-        x[i] = KIND == DK_INT8 ? f2_pack(static_cast<float>(static_cast<int>(lo)), static_cast<float>(static_cast<int>(hi)))
-                               : f2_pack(__uint_as_float(lo), __uint_as_float(hi));
-        const uint64_t b2 = f2_pack(bias[i % 2], bias[i % 2]);
-        if constexpr (KIND != DK_F16) {
-          if (p.sa) x[i] = f2_mul(x[i], sa[k + i / 2]);
-          x[i] = f2_fma(x[i], f2_pack(sw[i % 2], sw[i % 2]), b2);
-        } else {
-          x[i] = f2_add(x[i], b2);
+        for (int i = 0; i < 4; ++i) {
+          const int f = 2 * half + i % 2;
+          const uint32_t lo = v[c % 2][4 * kk + 2 * i], hi = v[c % 2][4 * kk + 2 * i + 1];
+          x[i] = KIND == DK_INT8 ? f2_pack(static_cast<float>(static_cast<int>(lo)), static_cast<float>(static_cast<int>(hi)))
+                                 : f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+          const uint64_t b2 = f2_pack(bias[f], bias[f]);
+          if constexpr (KIND != DK_F16) x[i] = f2_fma(f2_mul(x[i], sa[k0 + i / 2]), f2_pack(sw[f], sw[f]), b2);
+          else x[i] = f2_add(x[i], b2);
         }
-      }
-      if (p.act == DENSE_GELU) {
+        if (p.act == DENSE_GELU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = gelu_tanh2(x[i]);
-      } else if (p.act == DENSE_SILU) {
+          for (int i = 0; i < 4; ++i) x[i] = gelu_tanh2(x[i]);
+        } else if (p.act == DENSE_SILU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = silu2(x[i]);
-      }
-      if (p.gate) {
-        if (one_gate) {
+          for (int i = 0; i < 4; ++i) x[i] = silu2(x[i]);
+        }
+        if (p.gate) {
+          if (one_gate) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], f2_pack(gate[i % 2], gate[i % 2]));
-        } else {
+            for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], f2_pack(gate[2 * half + i % 2], gate[2 * half + i % 2]));
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {  // the pairs' first and second tokens
+              float g[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = i % 2 ? nb : na, m = m0 + 8 * (k + i / 2) + tc;
-            float g[2];
+              for (int i = 0; i < 4; ++i) {
+                const int n = n0 + 8 * (2 * half + i % 2) + (lane >> 2), m = m0 + 8 * (k0 + i / 2) + 2 * (lane & 3) + j;
+                g[i] = n < p.N && m < p.M ? to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>(m / p.gate_rows) * p.ldg + n)) : 0.f;
+              }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              g[j] = n < p.N && m + j < p.M
-                         ? to_f32<OUT>(__ldg(p.gate + static_cast<int64_t>((m + j) / p.gate_rows) * p.ldg + n)) : 0.f;
-            x[i] = f2_mul(x[i], f2_pack(g[0], g[1]));
+              for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], j ? f2_pack(1.f, g[i]) : f2_pack(g[i], 1.f));
+            }
           }
         }
-      }
-      const uint32_t at = box + swz_off(8 * k + mtok, 2 * half + mfeat, 64);
-      if (p.res) {
-        uint32_t r[4];
-        ldmatrix_x4_trans(at, r);
+        const uint32_t at = box + swz_off(8 * k0 + mtok, 2 * half + mfeat, 64);
+        if (p.res) {
+          uint32_t r[4];
+          ldmatrix_x4_trans(at, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = f2_add(x[i], f2_pack(to_f32<OUT>(static_cast<uint16_t>(r[i])), to_f32<OUT>(static_cast<uint16_t>(r[i] >> 16))));
-      }
-      uint32_t o[4];
+          for (int i = 0; i < 4; ++i)
+            x[i] = f2_add(x[i], f2_pack(to_f32<OUT>(static_cast<uint16_t>(r[i])), to_f32<OUT>(static_cast<uint16_t>(r[i] >> 16))));
+        }
+        uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack_out<OUT>(f2_lo(x[i]), f2_hi(x[i]));
-      stmatrix_x4_trans(at, o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 4; ++i) o[i] = pack_out<OUT>(f2_lo(x[i]), f2_hi(x[i]));
+        stmatrix_x4_trans(at, o[0], o[1], o[2], o[3]);
+      }
     }
   }
-}
+};
 
-template <int KIND, int OUT>
+// TILED: the tiled form; else p.store says which.
+template <int KIND, int OUT, bool TILED>
 __global__ void __launch_bounds__(DP_THREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                       const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * ac);
       };
-      if (p.store == STORE_TILED) {
+      if constexpr (TILED) {
         const bool on = n0 < p.N && m0 < p.M;
         if (lane == 0) bulk_wait_read();  // the previous tile has left the box
         if (p.res && on && lane == 0) {
@@ -514,6 +528,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
           tma_load_2d(box, &tm_r, res_full, n0, m0);
         }
         res_on = p.res && on;
+        DenseTileOut<KIND, OUT> out;
+        out.prepare(p, n0, m0, lane);
         if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
         tc_fence_after();
         if (on) {
@@ -522,16 +538,15 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
             res_ph ^= 1;
             res_on = false;
           }
-          dense_tile_out<KIND, OUT>(p, ta, box, n0, m0, lane);
-        }
-        acc_read();
-        if (on) {
+          out.run(p, ta, box, n0, m0, lane, acc_read);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             tma_store_2d(&tm_y, box, n0, m0);
             bulk_commit();
           }
+        } else {
+          acc_read();
         }
         continue;
       }
@@ -741,12 +756,12 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
           uint64_t x[8];
           tmem_ld_x16(ta + c, v);
           if (p.res) {
-            if (p.store >= STORE_PAIRED) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
+            if (p.store == STORE_PAIRED) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
             else dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
           }
           tmem_ld_wait();
           dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
-          if (p.store >= STORE_PAIRED) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
+          if (p.store == STORE_PAIRED) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
           else dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
         }
       }

@@ -251,16 +251,16 @@ constexpr int64_t kRopeMaxSpan = 1ll << 44;  // elements of a dimension's extent
 // ---------------------------------------------------------------------- dense
 // Clusters of two CTAs that fit on the device at once (cached per device,
 // stored + 1).
-template <int KIND, int OUT>
+template <int KIND, int OUT, bool TILED>
 int dense_pair_clusters(const DeviceInfo& d) {
   static std::atomic<int> cache[64];
   if (d.dev < 0 || d.dev >= 64) return 0;
   if (const int known = cache[d.dev].load(std::memory_order_acquire); known > 0) return known - 1;
   constexpr int smem = DensePairSmem::TOTAL;
-  if (ensure_smem<dense_pair_kernel<KIND, OUT>>(smem) != SVDQ_OK) return 0;
+  if (ensure_smem<dense_pair_kernel<KIND, OUT, TILED>>(smem) != SVDQ_OK) return 0;
   LaunchCfg lc(dim3(2 * (d.sms / 2)), dim3(DP_THREADS), smem, nullptr, 2);
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, OUT>, &lc.cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, OUT, TILED>, &lc.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;  // not cached: the next call asks again
   }
@@ -290,17 +290,16 @@ svdq_status dense_maps(const DenseCall& c, int wrows, int arows, CUtensorMap* tw
   return make_tmap(ta, c.d->a, dt, es, c.d->K, c.d->M, 128 / es, arows, CU_TENSOR_MAP_SWIZZLE_128B, c.lda);
 }
 
-template <int KIND, int OUT>
+template <int KIND, int OUT, bool TILED>
 svdq_status launch_dense_pair(DenseCall& c) {
   constexpr int BN = DensePairSmem::BN;
   constexpr int smem = DensePairSmem::TOTAL;
-  const int clusters = dense_pair_clusters<KIND, OUT>(c.dev);
+  const int clusters = dense_pair_clusters<KIND, OUT, TILED>(c.dev);
   if (clusters < 1) return SVDQ_ERR_CUDA;
   CUtensorMap tw, ta, ty, tr;
   if (svdq_status s = dense_maps<KIND, OUT>(c, 128, BN / 2, &tw, &ta); s != SVDQ_OK) return s;
   ty = tr = ta;  // not used unless the stores are tiled
-  if (c.tiled) {
-    c.p.store = STORE_TILED;
+  if constexpr (TILED) {
     constexpr CUtensorMapDataType dt = OUT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (svdq_status s = make_tmap(&ty, c.d->y, dt, 2, c.d->N, c.d->M, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B, 2 * c.d->ldy);
         s != SVDQ_OK)
@@ -314,7 +313,7 @@ svdq_status launch_dense_pair(DenseCall& c) {
   c.p.num_t = static_cast<int>(cdiv(c.p.M, BN));
   const int tiles = c.p.num_f * c.p.num_t;
   LaunchCfg lc(dim3(2 * std::min(tiles, clusters)), dim3(DP_THREADS), smem, c.st, 2);
-  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_pair_kernel<KIND, OUT>, tw, ta, ty, tr, c.p));
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_pair_kernel<KIND, OUT, TILED>, tw, ta, ty, tr, c.p));
   return SVDQ_OK;
 }
 
@@ -351,7 +350,7 @@ DenseChoice dense_choose(int64_t M, int64_t N, int kblk, int sms) {
 template <int KIND, int OUT>
 svdq_status launch_dense(DenseCall& c) {
   const DenseChoice v = dense_choose(c.p.M, c.p.N, c.p.kblk, c.dev.sms);
-  if (v.pair) return launch_dense_pair<KIND, OUT>(c);
+  if (v.pair) return c.tiled ? launch_dense_pair<KIND, OUT, true>(c) : launch_dense_pair<KIND, OUT, false>(c);
   switch (v.bn) {
     case 16: return launch_dense_solo<KIND, OUT, 16>(c, v.split);
     case 32: return launch_dense_solo<KIND, OUT, 32>(c, v.split);
