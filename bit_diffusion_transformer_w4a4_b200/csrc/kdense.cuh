@@ -45,6 +45,7 @@ struct DenseParams {
   int M, N;
   int kblk;               // 128-byte k-blocks
   int num_f, num_t;       // feature and token tiles
+  int split;              // CTAs (pairs) that share a tile's K range
   int act;
   int store;              // form of the stores and residual loads (below)
   int* err;               // or null
@@ -237,6 +238,36 @@ __device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLan
   }
 }
 
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// The sums over `split` CTAs (ranks step o + first) of a feature's NC
+// consecutive tokens at `addr` of each one's [token][128 features] partial
+// tile, in rank order: they do not depend on timing.
+template <int KIND, int NC>
+__device__ __forceinline__ void dense_join(uint32_t addr, int split, int step, int first, uint32_t* v) {
+  constexpr int G = 16 / NC;  // CTAs whose sums are fetched at a time
+#pragma unroll
+  for (int j = 0; j < NC; ++j) v[j] = 0;
+#pragma unroll 1
+  for (int o0 = 0; o0 < split; o0 += G) {
+    uint32_t w[G][NC];
+#pragma unroll
+    for (int o = 0; o < G; ++o) {
+      const uint32_t at = mapa_shared(addr, step * min(o0 + o, split - 1) + first);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) w[o][j] = o0 + o < split ? ld_cluster_u32(at + j * 512) : 0u;
+    }
+#pragma unroll
+    for (int o = 0; o < G; ++o)
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        v[j] = KIND == DK_INT8 ? v[j] + w[o][j] : __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[o][j]));
+  }
+}
+
 // ------------------------------------------------ pairs of SMs, large calls
 // A cluster of two CTAs owns 256 features x BN tokens: rank r loads weight
 // rows [128 r, 128 r + 128) and token rows [BN/2 r, BN/2 r + BN/2) of the
@@ -381,7 +412,9 @@ struct DenseTileOut {
   }
 };
 
-// TILED: the tiled form; else p.store says which.
+// TILED: the tiled form; else p.store says which.  p.split > 1 (not TILED):
+// a cluster of p.split pairs shares the K range of one tile, and the sums meet
+// in distributed shared memory as in the single-SM kernel.
 template <int KIND, int OUT, bool TILED>
 __global__ void __launch_bounds__(DP_THREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
@@ -405,9 +438,16 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int cid = static_cast<int>(blockIdx.x >> 1);
-  const int nclu = static_cast<int>(gridDim.x >> 1);
+  const int split = TILED ? 1 : p.split;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1, lead = crank & ~1u;  // rank in the pair; the pair's leader
+  const int pr = static_cast<int>(crank >> 1);          // this pair's slice of K
+  const int cid = static_cast<int>(blockIdx.x) / (2 * split);
+  const int nclu = static_cast<int>(gridDim.x) / (2 * split);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblk) * pr / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblk) * (pr + 1) / split);
+  const uint16_t both = static_cast<uint16_t>(0x3u << lead);
+  bool good = true;
   const Guard guard{p.err ? p.err : &g_dense_err, abort_flag, p.timeout_ns};
   const int num_tiles = p.num_f * p.num_t;
 
@@ -440,7 +480,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tm_w);
       tma_prefetch_desc(&tm_a);
-      const uint32_t full0 = mapa_shared(bar_full, 0);  // the leader's full barriers
+      const uint32_t full0 = mapa_shared(bar_full, lead);  // the leader's full barriers
       int s = 0;
       uint32_t ph = 0, issued = 0, issued_par = 0;
       bool ok = true;
@@ -449,7 +489,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         dense_tile(p, tile, ft, tt);
         const int wrow = ft * 256 + static_cast<int>(rank) * 128;
         const int arow = tt * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < p.kblk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait_bounded(bar_empty + 8 * s, ph ^ 1, guard, 0x301))) break;
           issued &= ~(1u << s);
           const uint32_t st = sbase + s * S::STAGE;
@@ -479,21 +519,21 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         const uint32_t d = tmem + ac * 256;
         if (j > 1 && !(ok = wait_bounded_cl(bar_acc_empty + 8 * ac, ((j >> 1) - 1) & 1, guard, 0x302))) break;
         tc_fence_after();
-        for (int kb = 0; kb < p.kblk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait_bounded(bar_full + 8 * s, ph, guard, 0x303))) break;
           tc_fence_after();
           const uint64_t so = kStage * s;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dense_mma<KIND, true>(d, dW0 + so + 2 * i, dA0 + so + 2 * i, id, (kb | i) != 0);
-          tc_commit_pair(bar_empty + 8 * s, 0x3);
+            dense_mma<KIND, true>(d, dW0 + so + 2 * i, dA0 + so + 2 * i, id, (kb != kb0) | (i != 0));
+          tc_commit_pair(bar_empty + 8 * s, both);
           if (++s == NST) { s = 0; ph ^= 1; }
         }
         if (!ok) break;
-        tc_commit_pair(bar_acc_full + 8 * ac, 0x3);
+        tc_commit_pair(bar_acc_full + 8 * ac, both);
       }
       // every MMA of the pair has completed before either CTA frees tensor memory
-      tc_commit_pair(bar_drain, 0x1);
+      tc_commit_pair(bar_drain, static_cast<uint16_t>(1u << lead));
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(bar_drain, 0) && global_timer_ns() - t0 < p.timeout_ns) {
       }
@@ -503,7 +543,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     constexpr int CW = BN / 4;           // tokens of this warp
     const int q = warp & 3;              // tensor-memory lane group of this warp
     const int c0 = (e >> 2) * CW;
-    const uint32_t acc_empty0 = mapa_shared(bar_acc_empty, 0);
+    const uint32_t acc_empty0 = mapa_shared(bar_acc_empty, lead);
     const uint32_t box = sbase + S::OUT_OFF + e * S::OUT_BYTES;
     const uint32_t res_full = bar_res + 8 * e;
     uint32_t res_ph = 0;
@@ -549,6 +589,22 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
           acc_read();
         }
         continue;
+      }
+      if (split > 1) {  // one tile per cluster: the partial sums take the stages' place
+        good = __all_sync(0xffffffffu, wait_bounded(bar_acc_full, 0, guard, 0x304, 64));
+        if (!good) break;
+        tc_fence_after();
+        uint32_t* part = reinterpret_cast<uint32_t*>(smem);
+#pragma unroll 1
+        for (int c = 0; c < CW; c += 32) {
+          uint32_t v[32];
+          tmem_ld_x32(ta + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[(c0 + c + i) * 128 + q * 32 + lane] = v[i];
+        }
+        acc_read();
+        break;
       }
       const int n = n0 + lane;
       DenseLane l = dense_lane<OUT>(p, n, m0);
@@ -601,6 +657,42 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     }
   }
 
+  if constexpr (!TILED) {
+    if (split > 1) {
+      __syncwarp();
+      cluster_sync();  // every pair's partial sums are in place
+      if (warp >= 4 && good) {
+        const int e = warp - 4, q = warp & 3;
+        int ft, tt;
+        dense_tile(p, cid, ft, tt);
+        const int f = q * 32 + lane, n = ft * 256 + static_cast<int>(rank) * 128 + f;
+        const int cols = BN / split / 4;  // tokens of this warp: 32 or 16
+        const int c0 = pr * (BN / split) + (e >> 2) * cols;
+        const int m0 = tt * BN + c0;
+        float* sa = reinterpret_cast<float*>(smem + S::OUT_OFF + e * S::OUT_BYTES);
+        if (KIND != DK_F16 && p.sa) {
+          if (lane < cols) sa[lane] = m0 + lane < p.M ? __ldg(p.sa + m0 + lane) : 0.f;
+          __syncwarp();
+        }
+        const float* sc = KIND != DK_F16 && p.sa ? sa : nullptr;
+        DenseLane l = dense_lane<OUT>(p, n, m0);
+#pragma unroll 1
+        for (int c = 0; c < cols && m0 + c < p.M; c += 16) {
+          uint32_t r[16], v[16];
+          if (p.res) {
+            if (p.store == STORE_PAIRED) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
+            else dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
+          }
+          dense_join<KIND, 16>(sbase + ((c0 + c) * 128 + f) * 4, split, 2, rank, v);
+          uint64_t x[8];
+          dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+          if (p.store == STORE_PAIRED) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
+          else dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
+        }
+      }
+    }
+  }
+  __syncwarp();
   tc_fence_before();
   cluster_sync();  // the pair's MMAs, loads and remote arrivals are all done
   if (warp == 1) {
@@ -630,16 +722,10 @@ struct DenseSoloSmem {
   static_assert(2 * TOTAL <= 232448, "shared memory of two CTAs");
 };
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 template <int KIND, int OUT, int BN>
 __global__ void __launch_bounds__(DS_THREADS, 2)
     dense_solo_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
-                      const __grid_constant__ DenseParams p, int split) {
+                      const __grid_constant__ DenseParams p) {
   using S = DenseSoloSmem<BN>;
   constexpr int NST = S::STAGES;
   constexpr int COLS = BN < 32 ? 32 : BN;
@@ -656,6 +742,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int split = p.split;
   const int rank = static_cast<int>(blockIdx.x) % split;
   const int tile = static_cast<int>(blockIdx.x) / split;
   const int ft = tile % p.num_f, tt = tile / p.num_f;
@@ -789,24 +876,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
         uint32_t v[2], r[2];
         uint64_t x[1];
         if (p.res) dense_residual<OUT, 2, false>(p, l, m0 + c, n, r);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t at = sbase + ((c + j) * 128 + f) * 4;
-          uint32_t w[8];
-#pragma unroll
-          for (int o = 0; o < 8; ++o) w[o] = o < split ? ld_cluster_u32(mapa_shared(at, o)) : 0u;
-          if constexpr (KIND == DK_INT8) {
-            int a = 0;
-#pragma unroll
-            for (int o = 0; o < 8; ++o) a += static_cast<int>(w[o]);
-            v[j] = static_cast<uint32_t>(a);
-          } else {
-            float a = 0.f;
-#pragma unroll
-            for (int o = 0; o < 8; ++o) a += __uint_as_float(w[o]);
-            v[j] = __float_as_uint(a);
-          }
-        }
+        dense_join<KIND, 2>(sbase + (c * 128 + f) * 4, split, 1, 0, v);
         dense_math<KIND, OUT, 2>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
         dense_store<OUT, 2, false>(p, l, m0 + c, n, x, r);
       }

@@ -291,7 +291,7 @@ svdq_status dense_maps(const DenseCall& c, int wrows, int arows, CUtensorMap* tw
 }
 
 template <int KIND, int OUT, bool TILED>
-svdq_status launch_dense_pair(DenseCall& c) {
+svdq_status launch_dense_pair(DenseCall& c, int split) {
   constexpr int BN = DensePairSmem::BN;
   constexpr int smem = DensePairSmem::TOTAL;
   const int clusters = dense_pair_clusters<KIND, OUT, TILED>(c.dev);
@@ -312,7 +312,8 @@ svdq_status launch_dense_pair(DenseCall& c) {
   c.p.num_f = static_cast<int>(cdiv(c.p.N, 256));
   c.p.num_t = static_cast<int>(cdiv(c.p.M, BN));
   const int tiles = c.p.num_f * c.p.num_t;
-  LaunchCfg lc(dim3(2 * std::min(tiles, clusters)), dim3(DP_THREADS), smem, c.st, 2);
+  c.p.split = split;
+  LaunchCfg lc(dim3(split > 1 ? 2 * split * tiles : 2 * std::min(tiles, clusters)), dim3(DP_THREADS), smem, c.st, 2 * split);
   SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_pair_kernel<KIND, OUT, TILED>, tw, ta, ty, tr, c.p));
   return SVDQ_OK;
 }
@@ -325,8 +326,9 @@ svdq_status launch_dense_solo(DenseCall& c, int split) {
   if (svdq_status s = dense_maps<KIND, OUT>(c, 128, BN, &tw, &ta); s != SVDQ_OK) return s;
   c.p.num_f = static_cast<int>(cdiv(c.p.N, 128));
   c.p.num_t = static_cast<int>(cdiv(c.p.M, BN));
+  c.p.split = split;
   LaunchCfg lc(dim3(static_cast<unsigned>(split) * c.p.num_f * c.p.num_t), dim3(DS_THREADS), smem, c.st, split);
-  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_solo_kernel<KIND, OUT, BN>, tw, ta, c.p, split));
+  SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, dense_solo_kernel<KIND, OUT, BN>, tw, ta, c.p));
   return SVDQ_OK;
 }
 
@@ -350,7 +352,9 @@ DenseChoice dense_choose(int64_t M, int64_t N, int kblk, int sms) {
 template <int KIND, int OUT>
 svdq_status launch_dense(DenseCall& c) {
   const DenseChoice v = dense_choose(c.p.M, c.p.N, c.p.kblk, c.dev.sms);
-  if (v.pair) return c.tiled ? launch_dense_pair<KIND, OUT, true>(c) : launch_dense_pair<KIND, OUT, false>(c);
+  if (v.pair) {
+    return c.tiled && v.split == 1 ? launch_dense_pair<KIND, OUT, true>(c, 1) : launch_dense_pair<KIND, OUT, false>(c, v.split);
+  }
   switch (v.bn) {
     case 16: return launch_dense_solo<KIND, OUT, 16>(c, v.split);
     case 32: return launch_dense_solo<KIND, OUT, 32>(c, v.split);
