@@ -248,7 +248,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // tile, in rank order: they do not depend on timing.
 template <int KIND, int NC>
 __device__ __forceinline__ void dense_join(uint32_t addr, int split, int step, int first, uint32_t* v) {
-  constexpr int G = 16 / NC;  // CTAs whose sums are fetched at a time
+  constexpr int G = NC == 2 ? 8 : 2;  // CTAs whose sums are fetched at a time
 #pragma unroll
   for (int j = 0; j < NC; ++j) v[j] = 0;
 #pragma unroll 1
@@ -869,16 +869,34 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
   if (split > 1) {
     cluster_sync();  // all partial tiles are in place
     if (warp >= 2 && ok) {
-      const int per = 2 * ((valid + 2 * split - 1) / (2 * split));  // even: two tokens at a time
+      // this CTA's tokens: 16 at a time where there are as many, else two
+      const int unit = valid >= 16 * split ? 16 : 2;
+      const int per = unit * ((valid + unit * split - 1) / (unit * split));
       const int c1 = min(valid, (rank + 1) * per);
       if (p.gate) l = dense_lane<OUT>(p, n, m0 + rank * per);
-      for (int c = rank * per; c < c1; c += 2) {
-        uint32_t v[2], r[2];
-        uint64_t x[1];
-        if (p.res) dense_residual<OUT, 2, false>(p, l, m0 + c, n, r);
-        dense_join<KIND, 2>(sbase + (c * 128 + f) * 4, split, 1, 0, v);
-        dense_math<KIND, OUT, 2>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
-        dense_store<OUT, 2, false>(p, l, m0 + c, n, x, r);
+      if (unit == 16) {
+#pragma unroll 1
+        for (int c = rank * per; c < c1; c += 16) {
+          uint32_t v[16], r[16];
+          uint64_t x[8];
+          if (p.res) {
+            if (p.store == STORE_PAIRED) dense_residual<OUT, 16, true>(p, l, m0 + c, n, r);
+            else dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
+          }
+          dense_join<KIND, 16>(sbase + (c * 128 + f) * 4, split, 1, 0, v);
+          dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+          if (p.store == STORE_PAIRED) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
+          else dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
+        }
+      } else {
+        for (int c = rank * per; c < c1; c += 2) {
+          uint32_t v[2], r[2];
+          uint64_t x[1];
+          if (p.res) dense_residual<OUT, 2, false>(p, l, m0 + c, n, r);
+          dense_join<KIND, 2>(sbase + (c * 128 + f) * 4, split, 1, 0, v);
+          dense_math<KIND, OUT, 2>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
+          dense_store<OUT, 2, false>(p, l, m0 + c, n, x, r);
+        }
       }
     }
     cluster_sync();  // no CTA leaves while its partial tile may be read
