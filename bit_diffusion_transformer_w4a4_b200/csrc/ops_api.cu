@@ -332,21 +332,54 @@ svdq_status launch_dense_solo(DenseCall& c, int split) {
   return SVDQ_OK;
 }
 
-// The variant of a call.
+// The variant of a call: tile size and K split, by the estimated time of each
+// in microseconds.  The model is what bounds the kernels: a fixed part, and
+// per wave of resident CTAs the K loop, whose block takes as long as the
+// latency of its loads over the stages in flight or as the bytes of the CTAs
+// that share an SM, whichever is more, plus the store of the tile; a split
+// adds its join, and clusters of four and eight leave some SMs without a CTA.
+// Its constants are fitted to 493 measured (M, N, K, type) with up to 19
+// variants each: the choice is within 2 % of the fastest variant on average
+// and within a third at worst.  What is lost by fixed choices: 512 x 2048 ->
+// 3072 takes 12.9 us in 128 x 64 tiles, 15.7 on pairs; 4608 x 3072 -> 3072
+// 61 on pairs, 80 in 128 x 128 tiles; 1 x 12288 -> 640 9.3 split in eight, 69
+// whole; 512 x 6144 -> 3072 25 on pairs split in two, 35 whole.
 struct DenseChoice {
   int pair;   // pairs of SMs
   int bn;     // tokens per tile
-  int split;  // CTAs that share a tile's K range
+  int split;  // CTAs or pairs that share a tile's K range
 };
 
 DenseChoice dense_choose(int64_t M, int64_t N, int kblk, int sms) {
-  const int64_t nf = cdiv(N, 128);
-  DenseChoice c{0, 16, 1};
-  if (cdiv(N, 256) * cdiv(M, 256) >= sms / 2) return DenseChoice{1, 256, 1};
-  while (c.bn < 128 && c.bn < M) c.bn *= 2;
-  while (c.bn > 16 && nf * cdiv(M, c.bn) < sms / 2) c.bn /= 2;
-  while (c.split < 8 && nf * cdiv(M, c.bn) * c.split * 2 <= 2 * sms && kblk >= 4 * c.split) c.split *= 2;
-  return c;
+  const float scale = static_cast<float>(sms) / 148.f;  // of the capacities, measured on 148 SMs
+  auto waves = [&](int64_t n, float cap) { return std::ceil(static_cast<float>(n) / std::max(1.f, cap * scale)); };
+  DenseChoice best{1, 256, 1};
+  float least = INFINITY;
+  auto offer = [&](DenseChoice c, float t) {
+    if (t < least) {
+      least = t;
+      best = c;
+    }
+  };
+  const int64_t pairs = cdiv(N, 256) * cdiv(M, 256);
+  for (int i = 0, s = 1; s <= 4; ++i, s *= 2) {
+    if (s > 1 && 2 * s > kblk) break;
+    constexpr float cap[3] = {74.f, 31.f, 15.f}, join[3] = {0.f, 1.4f, 2.9f};
+    offer({1, 256, s}, 5.0f + join[i] + waves(pairs, cap[i]) * (static_cast<float>(kblk) / s * 0.32f + 1.25f));
+  }
+  for (int i = 0, bn = 16; bn <= 128; ++i, bn *= 2) {
+    if (i > 0 && bn >= 2 * M) break;
+    const int64_t tiles = cdiv(N, 128) * cdiv(M, bn);
+    for (int j = 0, s = 1; s <= 8; ++j, s *= 2) {
+      if (s > 1 && 2 * s > kblk) break;
+      constexpr float latency[4] = {0.167f, 0.205f, 0.217f, 0.341f};  // a k-block, by bn
+      constexpr float cap[4] = {246.f, 296.f, 140.f, 127.f}, join[4] = {0.f, 1.4f, 0.9f, 0.7f};
+      const float here = std::min(static_cast<float>(tiles * s), cap[j] * scale) / sms;  // CTAs on an SM
+      const float block = std::max(latency[i], here * (16384 + bn * 128) / 143000.f);
+      offer({0, bn, s}, 4.6f + join[j] + waves(tiles * s, cap[j]) * (static_cast<float>(kblk) / s * block + 0.0106f * bn));
+    }
+  }
+  return best;
 }
 
 template <int KIND, int OUT>
@@ -427,7 +460,9 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
            (!d->residual || (aligned(d->residual, 2 * n) && (M == 1 || d->ldr % n == 0)));
   };
   c.p.store = N % 2 == 0 && rows_by(2) ? STORE_PAIRED : STORE_PLAIN;
-  c.tiled = M > 1 && rows_by(8) && (!d->residual || d->ldr > 0);
+  // a tensor store writes whole 16-byte pieces of a row, also across the end
+  // that its map gives it: N itself a multiple of them too
+  c.tiled = M > 1 && N % 8 == 0 && rows_by(8) && (!d->residual || d->ldr > 0);
   c.p.err = d->device_error;
   c.p.timeout_ns = kDefaultTimeoutNs;
   const bool bf = d->out == SVDQ_BF16;

@@ -114,6 +114,43 @@ def test_dense_large(M, N, K, kind, out, act, gate_rows, residual):
     _check(p, buf, K, kind, out)
 
 
+# (M, N, 128-byte blocks of K): one or more shapes for each tile size and K split
+VARIANTS = [
+    (3, 200, 2), (1, 9000, 24), (9, 300, 9), (5, 130, 17), (1000, 1000, 1), (17, 9000, 40), (1000, 100, 16), (257, 200, 16),
+    (4100, 130, 1), (33, 9000, 40), (2100, 120, 16), (700, 104, 16), (500, 4096, 1), (200, 9000, 16), (4100, 120, 24),
+    (1000, 120, 96), (1000, 4096, 1), (4100, 2600, 3), (300, 18000, 5), (500, 3001, 40), (510, 3000, 41), (130, 3001, 96),
+    (250, 3000, 97),
+]
+
+
+@pytest.mark.parametrize("ypad", [0, 1, 2, 7])
+@pytest.mark.parametrize("kind,out", [("bf16", "bf16"), ("e4m3", "fp16"), ("int8", "bf16")])
+@pytest.mark.parametrize("M,N,blocks", VARIANTS)
+def test_dense_variants(M, N, blocks, kind, out, ypad):
+    """Every tile size and K split, with every form of the stores: Y's rows on
+    16-byte, 4-byte and 2-byte boundaries; all epilogue terms; a gate whose
+    rows change inside a tile."""
+    K = blocks * (64 if kind == "bf16" else 128) - (8 if kind == "bf16" else 48)
+    p, buf = _problem(M, N, K, kind, out, "gelu" if ypad % 2 else None, True, -(-M // 3) if M > 2 else 1, True, ypad=ypad)
+    svdq.dense_forward(**p)
+    _check(p, buf, K, kind, out)
+
+
+@pytest.mark.parametrize("M,N,blocks,ypad", [(4100, 2600, 3, 0), (510, 3000, 41, 0), (250, 3000, 97, 1), (300, 18001, 5, 7), (2000, 3000, 20, 0)])
+def test_dense_variants_in_place_twice(M, N, blocks, ypad):
+    """y = residual on the large variants, and equal bits from equal calls."""
+    K = 64 * blocks
+    p, buf = _problem(M, N, K, "bf16", "bf16", "silu", True, 100, True, ypad=ypad)
+    ref = _reference(p, K, "bf16", "bf16")
+    svdq.dense_forward(**p)
+    first = p["y"].clone()
+    p["y"].copy_(p["residual"])
+    p["residual"] = p["y"]
+    svdq.dense_forward(**p)
+    _check(p, buf, K, "bf16", "bf16", ref)
+    assert torch.equal(first, p["y"])
+
+
 @pytest.mark.parametrize("K", [1, 7, 63, 64, 65, 127, 128, 129, 1023])
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 def test_dense_k_tails(K, kind):
