@@ -369,8 +369,6 @@ def untile_nvfp4_scales(buf: np.ndarray, M: int, K: int) -> np.ndarray:
 # the tensors' own device, on `stream` or that device's current stream.
 BF16, FP16, FP32, E4M3, INT8 = range(5)
 ACTS = {None: 0, "none": 0, "gelu": 1, "silu": 2}
-_DTYPES: dict = {}
-_POS_TYPES: dict = {}
 
 
 class DenseDesc(ctypes.Structure):
@@ -424,36 +422,57 @@ _ROPE_POS = struct.Struct("@Pi4x3q")
 _ROPE_TENSOR = struct.Struct("@2P7q")
 
 
-def _dtypes() -> dict:
-    if not _DTYPES:
+class _Torch:
+    """What the calls need of torch, looked up once (importing this module
+    does not import torch)."""
+
+    def __init__(self):
         import torch
-        _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
-                        torch.float8_e4m3fn: E4M3, torch.int8: INT8})
-    return _DTYPES
+        self.dtypes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
+                       torch.float8_e4m3fn: E4M3, torch.int8: INT8}
+        self.pos_types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+        self.f32, self.i32 = torch.float32, torch.int32
+        self.device, self.available = torch.cuda.device, torch.cuda.is_available
+        if self.available():
+            torch.cuda.init()
+            self.current = torch._C._cuda_getDevice
+            self.raw_stream = torch._C._cuda_getCurrentRawStream
+        else:
+            self.current = lambda: None
 
 
-def _dtype(t, allowed, what: str) -> int:
-    d = _dtypes().get(t.dtype)
+_TORCH = None
+
+
+def _torch() -> _Torch:
+    global _TORCH
+    if _TORCH is None:
+        _TORCH = _Torch()
+    return _TORCH
+
+
+def _dtype(T, t, allowed, what: str) -> int:
+    d = T.dtypes.get(t.dtype)
     if d not in allowed:
         raise TypeError(f"{what}: dtype {t.dtype} is not supported here")
     return d
 
 
-def _differs(t, shape, dtype, dev, what: str):
+def _differs(t, shape, dtype, what: str):
     """Raise for the first of t's shape, dtype and device that is not as given."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
     raise ValueError(f"{what} is on {t.device}, expected the other tensors' device")
 
 
-def _matrix(t, rows, cols, dtype, dev, what: str) -> int:
-    """Row distance of a [rows x cols] tensor with contiguous rows."""
-    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev:
-        _differs(t, (rows, cols), dtype, dev, what)
+def _matrix(t, shape, dtype, dev, what: str) -> int:
+    """Row distance of a matrix with contiguous rows."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _differs(t, shape, dtype, what)
     ld, step = t.stride()
-    if step != 1 and cols > 1:
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
     return ld
 
@@ -461,7 +480,7 @@ def _matrix(t, rows, cols, dtype, dev, what: str) -> int:
 def _vector(t, n, dtype, dev, what: str) -> int:
     """Address of a contiguous [n] tensor."""
     if t.shape != (n,) or t.dtype is not dtype or t.get_device() != dev:
-        _differs(t, (n,), dtype, dev, what)
+        _differs(t, (n,), dtype, what)
     if n > 1 and t.stride() != (1,):
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
@@ -476,20 +495,17 @@ def _rows_of(t, rows_each, M, cols, dtype, dev, what: str):
     rows_each = int(rows_each) or max(M, 1)
     if rows_each < 1:
         raise ValueError(f"{what}: rows each must be positive")
-    return _matrix(t, -(-M // rows_each), cols, dtype, dev, what), rows_each
+    return _matrix(t, (-(-M // rows_each), cols), dtype, dev, what), rows_each
 
 
-def _run_on(dev: int, stream, call, *args) -> int:
-    """call(*args, stream) with CUDA device `dev` current."""
-    import torch
+def _run_on(T, dev: int, stream, call, *args) -> int:
+    """call(*args, stream) where CUDA device `dev` is not the current one."""
     if dev < 0:
-        if torch.cuda.is_available():
+        if T.available():
             raise ValueError("the tensors are on the CPU, expected a CUDA device")
         return call(*args, 0 if stream is None else int(stream))   # the library reports the missing device
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream))
-    return call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream))
+    with T.device(dev):
+        return call(*args, T.raw_stream(dev) if stream is None else int(stream))
 
 
 def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate=None, gate_rows=0,
@@ -502,36 +518,43 @@ def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate
     where that is one of them).  a_scale [M] and w_scale [N] are fp32 and for
     8-bit operands only.  act: None, "gelu" (tanh form) or "silu".  gate is [N]
     or [ceil(M / gate_rows), N].  residual may be y."""
-    kind, out = _dtype(a, (BF16, FP16, E4M3, INT8), "a"), _dtype(y, (BF16, FP16), "y")
-    if a.dim() != 2 or w.dim() != 2:
+    T = _TORCH or _torch()
+    kind, out = _dtype(T, a, (BF16, FP16, E4M3, INT8), "a"), _dtype(T, y, (BF16, FP16), "y")
+    sa, sw = a.shape, w.shape
+    if len(sa) != 2 or len(sw) != 2:
         raise ValueError("a and w must be matrices")
     if act not in ACTS:
         raise ValueError(f"act: {act!r}, expected one of {list(ACTS)}")
-    M, K = a.shape
-    N = w.shape[0]
+    M, K = sa
+    N = sw[0]
     dev, it, ot = a.get_device(), a.dtype, y.dtype
-    lda, ldw = _matrix(a, M, K, it, dev, "a"), _matrix(w, N, K, it, dev, "w")
-    ldy = _matrix(y, M, N, ot, dev, "y")
+    shape = (M, N)
+    lda, step = a.stride()
+    if step != 1 and K > 1:
+        raise ValueError("a: the elements of a row must be contiguous")
+    ldw, ldy = _matrix(w, (N, K), it, dev, "w"), _matrix(y, shape, ot, dev, "y")
     sa = sw = pb = pg = pr = pe = ldg = ldr = 0
-    if a_scale is not None or w_scale is not None or device_error is not None:
-        import torch
-        if a_scale is not None:
-            sa = _vector(a_scale, M, torch.float32, dev, "a_scale")
-        if w_scale is not None:
-            sw = _vector(w_scale, N, torch.float32, dev, "w_scale")
-        if device_error is not None:
-            pe = _vector(device_error, 1, torch.int32, dev, "device_error")
+    if a_scale is not None:
+        sa = _vector(a_scale, M, T.f32, dev, "a_scale")
+    if w_scale is not None:
+        sw = _vector(w_scale, N, T.f32, dev, "w_scale")
+    if device_error is not None:
+        pe = _vector(device_error, 1, T.i32, dev, "device_error")
     if bias is not None:
         pb = _vector(bias, N, ot, dev, "bias")
     if gate is not None:
         ldg, gate_rows = _rows_of(gate, gate_rows, M, N, ot, dev, "gate")
         pg = gate.data_ptr()
     if residual is not None:
-        ldr = _matrix(residual, M, N, ot, dev, "residual")
+        ldr = _matrix(residual, shape, ot, dev, "residual")
         pr = residual.data_ptr()
     d = _DENSE.pack(kind, out, ACTS[act], M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, sa, sw, pb, pg, ldg, gate_rows,
                     pr, ldr, y.data_ptr(), ldy, pe)
-    code = _run_on(dev, stream, lib().svdq_dense_forward, d)
+    call = (_LIB or lib()).svdq_dense_forward
+    if dev == T.current():
+        code = call(d, T.raw_stream(dev) if stream is None else int(stream))
+    else:
+        code = _run_on(T, dev, stream, call, d)
     if code:
         raise SvdqError(code, "svdq_dense_forward")
     return y
@@ -546,27 +569,35 @@ def rms_quantize8(x, codes, scales, residual=None, h=None, weight=None, weight_r
     float8_e4m3fn or int8, scales [M] fp32.  weight is [K] or
     [ceil(M / weight_rows), K].  residual, h and weight may be None; h may be x
     or residual.  Returns (codes, scales)."""
-    import torch
-    kind, out = _dtype(x, (BF16, FP16, FP32), "x"), _dtype(codes, (E4M3, INT8), "codes")
-    if x.dim() != 2:
+    T = _TORCH or _torch()
+    kind, out = _dtype(T, x, (BF16, FP16, FP32), "x"), _dtype(T, codes, (E4M3, INT8), "codes")
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be a matrix")
-    M, K = x.shape
+    M, K = shape
     dev, it = x.get_device(), x.dtype
-    ldx, ldc = _matrix(x, M, K, it, dev, "x"), _matrix(codes, M, K, codes.dtype, dev, "codes")
-    ps = _vector(scales, M, torch.float32, dev, "scales")
+    ldx, step = x.stride()
+    if step != 1 and K > 1:
+        raise ValueError("x: the elements of a row must be contiguous")
+    ldc = _matrix(codes, shape, codes.dtype, dev, "codes")
+    ps = _vector(scales, M, T.f32, dev, "scales")
     pr = ph = pw = ldr = ldh = ldw = 0
     if residual is not None:
-        ldr = _matrix(residual, M, K, it, dev, "residual")
+        ldr = _matrix(residual, shape, it, dev, "residual")
         pr = residual.data_ptr()
     if h is not None:
-        ldh = _matrix(h, M, K, it, dev, "h")
+        ldh = _matrix(h, shape, it, dev, "h")
         ph = h.data_ptr()
     if weight is not None:
         ldw, weight_rows = _rows_of(weight, weight_rows, M, K, it, dev, "weight")
         pw = weight.data_ptr()
     d = _RMS8.pack(kind, out, M, K, x.data_ptr(), ldx, pr, ldr, ph, ldh, pw, ldw, weight_rows, 1 if norm else 0, eps,
                    codes.data_ptr(), ldc, ps)
-    code = _run_on(dev, stream, lib().svdq_rms_quantize8, d)
+    call = (_LIB or lib()).svdq_rms_quantize8
+    if dev == T.current():
+        code = call(d, T.raw_stream(dev) if stream is None else int(stream))
+    else:
+        code = _run_on(T, dev, stream, call, d)
     if code:
         raise SvdqError(code, "svdq_rms_quantize8")
     return codes, scales
@@ -583,7 +614,7 @@ class RopeAxes:
         axes are sections of one line of frequencies."""
         dims = [int(v) for v in axis_dims]
         thetas = [float(v) for v in theta] if isinstance(theta, (list, tuple)) else [float(theta)] * max(1, len(dims))
-        self.head_dim, self.axis_dims, self.handle = int(head_dim), dims, None
+        self.head_dim, self.axis_dims, self.axes, self.handle = int(head_dim), dims, len(dims), None
         if len(dims) > 4 or len(thetas) != max(1, len(dims)):
             raise SvdqError(2, "svdq_rope_load")
         d = RopeDesc(self.head_dim, len(dims), (ctypes.c_int64 * 4)(*dims), (ctypes.c_double * 4)(*thetas),
@@ -593,17 +624,14 @@ class RopeAxes:
         _check(self._lib.svdq_rope_load(ctypes.byref(d), ctypes.byref(h)), "svdq_rope_load")
         self.handle = h
 
-    def _positions(self, pos, B, S, dev):
+    def _positions(self, T, pos, B, S, dev):
         """pos [S, axes] (shared by the sequences), [B, S, axes] or [B * S, axes]."""
-        if not _POS_TYPES:
-            import torch
-            _POS_TYPES.update({torch.int32: 0, torch.int64: 1, torch.float32: 2})
-        kind = _POS_TYPES.get(pos.dtype)
+        kind = T.pos_types.get(pos.dtype)
         if kind is None:
             raise TypeError(f"pos: dtype {pos.dtype} is not supported here")
         if pos.get_device() != dev:
             raise ValueError(f"pos is on {pos.device}, expected the other tensors' device")
-        n, shape, st = len(self.axis_dims), pos.shape, pos.stride()
+        n, shape, st = self.axes, pos.shape, pos.stride()
         if shape == (B * S, n):
             return _ROPE_POS.pack(pos.data_ptr(), kind, S * st[0], st[0], st[1])
         if shape == (S, n):
@@ -621,11 +649,11 @@ class RopeAxes:
         if not good:
             raise ValueError(f"{what}: shape {tuple(shape)} does not fit {B} sequences of {S} tokens with heads of {self.head_dim}")
         if x.dtype is not dtype or x.get_device() != dev:
-            _differs(x, tuple(shape), dtype, dev, what)
+            _differs(x, shape, dtype, what)
         if out is None:
             out = x
         elif out.shape != shape or out.dtype is not dtype or out.get_device() != dev:
-            _differs(out, tuple(shape), dtype, dev, what + "_out")
+            _differs(out, shape, dtype, what + "_out")
         st, so = x.stride(), out.stride()
         if st[-1] != 1 or so[-1] != 1:
             raise ValueError(f"{what}: the elements of a head must be contiguous")
@@ -639,7 +667,8 @@ class RopeAxes:
         place); ``inverse`` turns back, which is the gradient.  pos is int32,
         int64 or fp32: [S, axes] (shared), [B * S, axes] or [B, S, axes].
         Returns q's output, or both."""
-        kind = _dtype(q, (BF16, FP16, FP32), "q")
+        T = _TORCH or _torch()
+        kind = _dtype(T, q, (BF16, FP16, FP32), "q")
         shape = q.shape
         if len(shape) not in (3, 4):
             raise ValueError(f"q: shape {tuple(shape)}, expected [(B,) S, H, {self.head_dim}]")
@@ -648,8 +677,13 @@ class RopeAxes:
         tq, q_out = self._tensor(q, q_out, B, S, dtype, dev, "q")
         if k is not None:
             tk, k_out = self._tensor(k, k_out, B, S, dtype, dev, "k")
-        p = self._positions(pos, B, S, dev)
-        code = _run_on(dev, stream, self._lib.svdq_rope_apply, self.handle, kind, B, S, p, tq, tk, 1 if inverse else 0)
+        p = self._positions(T, pos, B, S, dev)
+        call = self._lib.svdq_rope_apply
+        if dev == T.current():
+            code = call(self.handle, kind, B, S, p, tq, tk, 1 if inverse else 0,
+                        T.raw_stream(dev) if stream is None else int(stream))
+        else:
+            code = _run_on(T, dev, stream, call, self.handle, kind, B, S, p, tq, tk, 1 if inverse else 0)
         if code:
             raise SvdqError(code, "svdq_rope_apply")
         return q_out if k is None else (q_out, k_out)
@@ -658,15 +692,15 @@ class RopeAxes:
         """(cos, sin) of every token and pair into ``table`` (contiguous fp32 of
         tokens x R elements), the ``rope`` argument of ``linear_forward_qkv``
         when R = 128.  pos is [tokens, axes]."""
-        import torch
+        T = _torch()
         if pos.dim() != 2:
             raise ValueError(f"pos: shape {tuple(pos.shape)}, expected [tokens, {len(self.axis_dims)}]")
         S = pos.shape[0]
-        if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() != S * sum(self.axis_dims):
+        if table.dtype != T.f32 or not table.is_contiguous() or table.numel() != S * sum(self.axis_dims):
             raise ValueError(f"table: expected {S * sum(self.axis_dims)} contiguous fp32 elements")
         dev = table.get_device()
-        p = self._positions(pos, 1, S, dev)
-        _check(_run_on(dev, stream, self._lib.svdq_rope_table, self.handle, 1, S, p, table.data_ptr()), "svdq_rope_table")
+        p = self._positions(T, pos, 1, S, dev)
+        _check(_run_on(T, dev, stream, self._lib.svdq_rope_table, self.handle, 1, S, p, table.data_ptr()), "svdq_rope_table")
         return table
 
     def close(self) -> None:
