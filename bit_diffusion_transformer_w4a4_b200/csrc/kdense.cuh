@@ -275,8 +275,8 @@ __device__ __forceinline__ void dense_join(uint32_t addr, int split, int step, i
 // its 128 features x BN tokens.  Persistent over tiles; two accumulators in
 // tensor memory, so the epilogue of one tile runs under the MMAs of the next.
 // Warps: 0 TMA, 1 MMA and tensor memory, 2-3 idle, 4-19 epilogue: each of the
-// 16 takes 32 features x 64 tokens.  In the tiled form a warp has a 4 KB box of
-// its own in shared memory: the residual arrives in it by a tensor load while
+// 16 takes 32 features x 64 tokens.  In the tiled form two warps (64 features,
+// a full line of Y) have a box of 8 KB in shared memory: the residual arrives in it by a tensor load while
 // the tile is being summed, the accumulator is read in the matrix-fragment
 // layout, stmatrix transposes the rounded result into the box in place, and a
 // tensor store takes it from there.  That is an eighth of an instruction per
@@ -292,9 +292,9 @@ struct DensePairSmem {
   static constexpr int STAGE = W_BYTES + A_BYTES;
   static constexpr int STAGES = 5;
   static constexpr uint32_t TX = 2 * STAGE;
-  static constexpr int OUT_OFF = STAGES * STAGE;            // [16 warps][64 tokens][32 features], 64-byte swizzle
-  static constexpr int OUT_BYTES = 64 * 32 * 2;
-  static constexpr int BAR_OFF = OUT_OFF + DP_EPI_WARPS * OUT_BYTES;
+  static constexpr int OUT_OFF = STAGES * STAGE;            // [8 pairs of warps][64 tokens][64 features], 128-byte swizzle
+  static constexpr int OUT_BYTES = 64 * 64 * 2;
+  static constexpr int BAR_OFF = OUT_OFF + DP_EPI_WARPS / 2 * OUT_BYTES;
   static constexpr int TOTAL = BAR_OFF + 512 + 1024;
   static_assert(TOTAL <= 232448, "shared memory per CTA");
 };
@@ -340,10 +340,11 @@ struct DenseTileOut {
     }
   }
 
-  // box: the warp's shared memory, holding the residual if there is one.
+  // box: the warps' shared memory, holding the residual if there is one; q: the
+  // warp's half of its features is q % 2.
   // `done` is called when the accumulator has been read.
   template <class F>
-  __device__ __forceinline__ void run(const DenseParams& p, uint32_t taddr, uint32_t box, int n0, int m0, int lane, F done) const {
+  __device__ __forceinline__ void run(const DenseParams& p, uint32_t taddr, uint32_t box, int q, int n0, int m0, int lane, F done) const {
     // lane 8 i + j of a matrix access: token j of column block i / 2, feature block i % 2
     const int mtok = ((lane >> 4) << 3) + (lane & 7), mfeat = (lane >> 3) & 1;
     uint32_t v[2][16];
@@ -395,7 +396,7 @@ struct DenseTileOut {
             }
           }
         }
-        const uint32_t at = box + swz_off(8 * k0 + mtok, 2 * half + mfeat, 64);
+        const uint32_t at = box + swz_off(8 * k0 + mtok, 4 * (q & 1) + 2 * half + mfeat, 128);
         if (p.res) {
           uint32_t r[4];
           ldmatrix_x4_trans(at, r);
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
   const uint32_t bar_acc_empty = smem_u32(bars + 2 * NST + 2);  // two, the leader's count
   const uint32_t bar_drain = smem_u32(bars + 2 * NST + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 5);
-  const uint32_t bar_res = smem_u32(bars + 2 * NST + 6);        // one per epilogue warp
+  const uint32_t bar_res = smem_u32(bars + 2 * NST + 6);        // one per pair of epilogue warps
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
       mbar_init(bar_acc_empty + 8 * i, 2 * DP_EPI_WARPS);
     }
     mbar_init(bar_drain, 1);
-    for (int i = 0; i < DP_EPI_WARPS; ++i) mbar_init(bar_res + 8 * i, 1);
+    for (int i = 0; i < DP_EPI_WARPS / 2; ++i) mbar_init(bar_res + 8 * i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -544,8 +545,10 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     const int q = warp & 3;              // tensor-memory lane group of this warp
     const int c0 = (e >> 2) * CW;
     const uint32_t acc_empty0 = mapa_shared(bar_acc_empty, lead);
-    const uint32_t box = sbase + S::OUT_OFF + e * S::OUT_BYTES;
-    const uint32_t res_full = bar_res + 8 * e;
+    const int b = (e >> 2) * 2 + (q >> 1);  // the box shared with the other warp of its 64 features
+    const uint32_t box = sbase + S::OUT_OFF + b * S::OUT_BYTES;
+    const uint32_t res_full = bar_res + 8 * b;
+    const bool first = (q & 1) == 0 && lane == 0;  // issues the box's tensor copies
     uint32_t res_ph = 0;
     bool res_on = false;                 // a residual load is in flight
     for (int tile = cid, j = 0; tile < num_tiles; tile += nclu, ++j) {
@@ -561,28 +564,31 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * ac);
       };
       if constexpr (TILED) {
-        const bool on = n0 < p.N && m0 < p.M;
-        if (lane == 0) bulk_wait_read();  // the previous tile has left the box
-        if (p.res && on && lane == 0) {
+        const int nb = n0 - 32 * (q & 1);  // the box's first feature
+        const bool on = nb < p.N && m0 < p.M;
+        if (first) bulk_wait_read();       // the previous tile has left the box
+        if (p.res && on && first) {
           mbar_expect_tx(res_full, S::OUT_BYTES);
-          tma_load_2d(box, &tm_r, res_full, n0, m0);
+          tma_load_2d(box, &tm_r, res_full, nb, m0);
         }
         res_on = p.res && on;
         DenseTileOut<KIND, OUT> out;
         out.prepare(p, n0, m0, lane);
-        if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64))) break;
+        bool ok = wait_bounded(bar_acc_full + 8 * ac, (j >> 1) & 1, guard, 0x304, 64);
+        if (ok && res_on) {
+          ok = wait_bounded(res_full, res_ph, guard, 0x305);
+          if (ok) res_ph ^= 1;
+          res_on = !ok;
+        }
+        // both warps of a box go on or give up together; the box is free
+        if (!named_barrier_all(1 + b, 64, ok)) break;
         tc_fence_after();
         if (on) {
-          if (p.res) {
-            if (!__all_sync(0xffffffffu, wait_bounded(res_full, res_ph, guard, 0x305))) break;
-            res_ph ^= 1;
-            res_on = false;
-          }
-          out.run(p, ta, box, n0, m0, lane, acc_read);
+          out.run(p, ta, box, q, n0, m0, lane, acc_read);
           fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tm_y, box, n0, m0);
+          named_barrier(1 + b, 64);        // both warps have written
+          if (first) {
+            tma_store_2d(&tm_y, box, nb, m0);
             bulk_commit();
           }
         } else {
@@ -608,8 +614,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
       }
       const int n = n0 + lane;
       DenseLane l = dense_lane<OUT>(p, n, m0);
-      // the box holds this warp's token scales
-      float* sa = reinterpret_cast<float*>(smem + S::OUT_OFF + e * S::OUT_BYTES);
+      // the boxes hold the warps' token scales
+      float* sa = reinterpret_cast<float*>(smem + S::OUT_OFF) + e * CW;
       if (KIND != DK_F16 && p.sa) {
         __syncwarp();  // the previous tile's scales have been read
         for (int i = lane; i < CW; i += 32) sa[i] = m0 + i < p.M ? __ldg(p.sa + m0 + i) : 0.f;
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         }
       }
     }
-    if (lane == 0) {
+    if (first) {
       if (res_on) {  // given up with the residual on its way
         const uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(res_full, res_ph) && global_timer_ns() - t0 < p.timeout_ns) {
@@ -669,7 +675,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         const int cols = BN / split / 4;  // tokens of this warp: 32 or 16
         const int c0 = pr * (BN / split) + (e >> 2) * cols;
         const int m0 = tt * BN + c0;
-        float* sa = reinterpret_cast<float*>(smem + S::OUT_OFF + e * S::OUT_BYTES);
+        float* sa = reinterpret_cast<float*>(smem + S::OUT_OFF) + e * 64;
         if (KIND != DK_F16 && p.sa) {
           if (lane < cols) sa[lane] = m0 + lane < p.M ? __ldg(p.sa + m0 + lane) : 0.f;
           __syncwarp();

@@ -301,11 +301,11 @@ svdq_status launch_dense_pair(DenseCall& c, int split) {
   ty = tr = ta;  // not used unless the stores are tiled
   if constexpr (TILED) {
     constexpr CUtensorMapDataType dt = OUT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if (svdq_status s = make_tmap(&ty, c.d->y, dt, 2, c.d->N, c.d->M, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B, 2 * c.d->ldy);
+    if (svdq_status s = make_tmap(&ty, c.d->y, dt, 2, c.d->N, c.d->M, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, 2 * c.d->ldy);
         s != SVDQ_OK)
       return s;
     if (c.d->residual)
-      if (svdq_status s = make_tmap(&tr, c.d->residual, dt, 2, c.d->N, c.d->M, 32, 64, CU_TENSOR_MAP_SWIZZLE_64B, 2 * c.d->ldr);
+      if (svdq_status s = make_tmap(&tr, c.d->residual, dt, 2, c.d->N, c.d->M, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, 2 * c.d->ldr);
           s != SVDQ_OK)
         return s;
   }
