@@ -14,9 +14,13 @@
 //
 // Bound by memory: x and the residual are read once, h, the codes and the
 // scales written once.  The two statistics of a row cross the warps of its
-// CTA through shared memory behind a single barrier.  Two kernels:
-//   rms8_kernel       one CTA per row, any alignment: the row goes straight
-//                     into registers
+// CTA through shared memory behind a single barrier.  Three kernels:
+//   rms8_kernel       one CTA per row: the row goes straight into registers
+//   rms8_flat_kernel  the same for packed rows whose length is no multiple of
+//                     16 bytes: x, residual, h and codes are cut at the 16-byte
+//                     boundaries of the whole matrix and not of the row, which
+//                     all of them share; a row's first and last piece are
+//                     partial, and the weight is shifted into place
 //   rms8_ring_kernel  many 16-byte aligned rows: persistent CTAs whose next
 //                     rows are always on their way into a ring in shared
 //                     memory (bulk copies), so that loads do not pause while
@@ -24,6 +28,8 @@
 #pragma once
 
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "kg_common.cuh"
 
@@ -47,26 +53,19 @@ __device__ __forceinline__ typename ElemOf<DT>::type from_f32(float v) {
   else return v;
 }
 
-// VEC consecutive elements: 16 bytes at once, or one element.
+// VEC consecutive elements in one access of 16, 8, 4 bytes or one element.
 template <int DT, int VEC>
 struct Pack {
   using E = typename ElemOf<DT>::type;
+  static constexpr int BYTES = VEC * sizeof(E);
+  using V = std::conditional_t<BYTES == 16, uint4, std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4 && VEC == 2, uint32_t, E>>>;
   union {
-    uint4 q;
+    V q;
     E e[VEC];
   };
-  __device__ __forceinline__ void load(const E* p) {
-    if constexpr (VEC * sizeof(E) == 16) q = __ldcs(reinterpret_cast<const uint4*>(p));
-    else e[0] = __ldcs(p);
-  }
-  __device__ __forceinline__ void load_cached(const E* p) {
-    if constexpr (VEC * sizeof(E) == 16) q = __ldg(reinterpret_cast<const uint4*>(p));
-    else e[0] = __ldg(p);
-  }
-  __device__ __forceinline__ void store(E* p) const {
-    if constexpr (VEC * sizeof(E) == 16) *reinterpret_cast<uint4*>(p) = q;
-    else p[0] = e[0];
-  }
+  __device__ __forceinline__ void load(const E* p) { q = __ldcs(reinterpret_cast<const V*>(p)); }
+  __device__ __forceinline__ void load_cached(const E* p) { q = __ldg(reinterpret_cast<const V*>(p)); }
+  __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<V*>(p) = q; }
 };
 
 // Elements 2i and 2i + 1 as a pair of fp32, and back.
@@ -329,6 +328,136 @@ __global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
     Pack<DT, VEC> g;
     if (HW) g.load_cached(w + k);
     rms8_codes<DT, VEC, HW, I8>(a[c], g, inv, codes + k);
+  }
+}
+
+// ------------------------------------------- packed rows of any length
+// VEC elements from index `at` of a row of K (others give 0).
+template <int DT, int VEC>
+__device__ __forceinline__ void load_within(Pack<DT, VEC>& v, const typename ElemOf<DT>::type* row, int at, int K) {
+  if (at >= 0 && at + VEC <= K) {
+    v.load_cached(row + at);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v.e[i] = at + i >= 0 && at + i < K ? __ldg(row + at + i) : typename ElemOf<DT>::type(0);
+  }
+}
+
+// Weights k .. k + VEC - 1 of an aligned row, where k + phase is a multiple of
+// VEC: two aligned pieces, shifted by the same amount in the whole CTA.
+template <int DT, int VEC>
+__device__ __forceinline__ void load_shifted(Pack<DT, VEC>& g, const typename ElemOf<DT>::type* w, int k, int phase, int K) {
+  Pack<DT, VEC> lo, hi;
+  load_within<DT, VEC>(lo, w, k + phase - VEC, K);
+  load_within<DT, VEC>(hi, w, k + phase, K);
+  uint32_t t[8] = {lo.q.x, lo.q.y, lo.q.z, lo.q.w, hi.q.x, hi.q.y, hi.q.z, hi.q.w};
+  const int s = VEC - phase;                       // 1 .. VEC elements
+  const int words = DT == DT_FP32 ? s : s / 2;     // 0 .. 4
+  if (words & 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = t[i + 4];
+  }
+  if (words & 2) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) t[i] = t[i + 2];
+  }
+  if (words & 1) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) t[i] = t[i + 1];
+  }
+  if (DT != DT_FP32 && (s & 1)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __byte_perm(t[i], t[i + 1], 0x5432);
+  }
+  g.q = make_uint4(t[0], t[1], t[2], t[3]);
+}
+
+// A piece at element k of a row; its elements outside the row are 0.
+template <int DT, int VEC>
+__device__ __forceinline__ void load_piece(Pack<DT, VEC>& v, const typename ElemOf<DT>::type* row, int k, int K) {
+  using E = typename ElemOf<DT>::type;
+  if (k >= 0 && k + VEC <= K) {
+    v.load(row + k);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v.e[i] = k + i >= 0 && k + i < K ? row[k + i] : E(0);
+  }
+}
+
+template <int DT, int CH, bool HW, bool I8>
+__global__ void __launch_bounds__(512, 1) rms8_flat_kernel(const RmsParams p) {
+  using E = typename ElemOf<DT>::type;
+  constexpr int VEC = 16 / sizeof(E);
+  __shared__ float red_s[32];
+  __shared__ uint32_t red_m[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t row = blockIdx.x;
+  const int nt = blockDim.x;
+  const int nw = nt >> 5;
+  const E* x = static_cast<const E*>(p.x) + row * p.ldx;
+  const E* r = static_cast<const E*>(p.res) + row * p.ldr;
+  E* h = static_cast<E*>(p.h) + row * p.ldh;
+  const E* w = static_cast<const E*>(p.w) + (HW && p.w_rows ? row / p.w_rows * p.ldw : 0);
+  uint8_t* codes = p.codes + row * p.ldc;
+  const int phase = static_cast<int>(row * p.ldx & (VEC - 1));  // the row starts this far into a piece
+  auto first = [&](int c) { return (c * nt + static_cast<int>(threadIdx.x)) * VEC - phase; };  // element of piece c
+
+  Pack<DT, VEC> a[CH], g[HW ? CH : 1];  // shifting the weight costs more than keeping it
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+    if (first(c) < p.K) load_piece(a[c], x, first(c), p.K);
+  if (p.res) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (first(c) < p.K) {
+        Pack<DT, VEC> b;
+        load_piece(b, r, first(c), p.K);
+        add_to(a[c], b);
+      }
+    }
+  }
+  RmsStats st;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int k = first(c);
+    if (k < p.K) {
+      if (p.h) {
+        if (k >= 0 && k + VEC <= p.K) {
+          a[c].store(h + k);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (k + i >= 0 && k + i < p.K) h[k + i] = a[c].e[i];
+        }
+      }
+      if (HW) load_shifted<DT, VEC>(g[HW ? c : 0], w, k, phase, p.K);
+      rms8_stats<DT, VEC, HW>(p, a[c], g[HW ? c : 0], st);
+    }
+  }
+  float ss;
+  uint32_t top;
+  rms8_join(st, ss, top, red_s, red_m, nw);
+  const float inv = rms8_scale(p, row, ss, top, [&] {
+    float s2 = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (first(c) < p.K) s2 = rms8_squares_down<DT, VEC>(a[c], s2);
+    return block_sum(s2, red_s, nw);
+  });
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int k = first(c);
+    if (k >= p.K) continue;
+    if (k >= 0 && k + VEC <= p.K) {
+      rms8_codes<DT, VEC, HW, I8>(a[c], g[HW ? c : 0], inv, codes + k);
+    } else {
+      __align__(8) uint8_t q[VEC];
+      rms8_codes<DT, VEC, HW, I8>(a[c], g[HW ? c : 0], inv, q);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (k + i >= 0 && k + i < p.K) codes[k + i] = q[i];
+    }
   }
 }
 

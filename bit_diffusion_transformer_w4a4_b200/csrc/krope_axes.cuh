@@ -16,8 +16,8 @@
 // present one, and every thread uses the (cos, sin) of its own elements for
 // all heads of Q and K, so the fp64 work is paid per token and not per head.
 //
-// Bound by memory: every element is read once and written once, in 16-byte
-// pieces where the layout allows (else one pair per thread).
+// Bound by memory: every element is read once and written once, in pieces of
+// 16, 8 or 4 bytes as the layout allows (else element by element).
 #pragma once
 
 #include "krms8.cuh"
@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(ROPE_THREADS, ROPE_CTAS) rope_axes_kernel(cons
   using E = typename ElemOf<DT>::type;
   constexpr bool TWO = !INTER || VEC == 1;                   // a unit's pairs span two pieces
   constexpr int NP = TWO ? VEC : VEC / 2;                    // pairs per rotating unit
-  constexpr int HB = TWO ? 2 : 4;
+  constexpr int BYTES = VEC * sizeof(E);
+  constexpr int HB = TWO ? (BYTES >= 16 ? 2 : BYTES >= 8 ? 4 : 8) : (BYTES >= 16 ? 4 : BYTES >= 8 ? 8 : 16);  // heads in flight
   __shared__ __align__(16) float cosines[2][ROPE_TOKENS][ROPE_MAX_PAIRS], sines[2][ROPE_TOKENS][ROPE_MAX_PAIRS];
   __shared__ double freq[ROPE_MAX_PAIRS];
   __shared__ uint8_t axis[ROPE_MAX_PAIRS];

@@ -113,6 +113,30 @@ svdq_status launch_rms_v(const RmsParams& p, int64_t M, int sms, cudaStream_t st
   return SVDQ_ERR_SHAPE;
 }
 
+// Packed rows of any length (see rms8_flat_kernel).
+template <int DT, int CH>
+svdq_status launch_rms_flat_t(const RmsParams& p, int64_t M, int nt, cudaStream_t st) {
+  LaunchCfg lc(dim3(static_cast<unsigned>(M)), dim3(nt), 0, st);
+  return rms_kinds(p, [&](auto hw, auto i8) -> svdq_status {
+    SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_flat_kernel<DT, CH, hw.value, i8.value>, p));
+    return SVDQ_OK;
+  });
+}
+
+template <int DT>
+svdq_status launch_rms_flat(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
+  constexpr int V = DT == DT_FP32 ? 4 : 8;
+  const int64_t pieces = cdiv(p.K + V - 1, V);  // a row may start inside one
+  const int64_t want = M <= 2 * sms ? 1 : pieces <= 256 ? 2 : 4;
+  const int64_t ch = std::max(want, cdiv(pieces, 512));
+  auto threads = [&](int c) { return static_cast<int>(cdiv(cdiv(pieces, c), 32) * 32); };
+  if (ch <= 1) return launch_rms_flat_t<DT, 1>(p, M, threads(1), st);
+  if (ch <= 2) return launch_rms_flat_t<DT, 2>(p, M, threads(2), st);
+  if (ch <= 4) return launch_rms_flat_t<DT, 4>(p, M, threads(4), st);
+  if (ch <= 8) return launch_rms_flat_t<DT, 8>(p, M, threads(8), st);
+  return launch_rms_v<DT, 1>(p, M, sms, st);
+}
+
 // Many aligned rows (see rms8_ring_kernel).
 template <int DT, int CH, bool HW, bool I8>
 svdq_status launch_rms_ring_k(const RmsParams& p, int64_t M, int sms, int nt, cudaStream_t st) {
@@ -163,7 +187,13 @@ svdq_status launch_rms(const RmsParams& p, int64_t M, int sms, cudaStream_t st) 
   const bool vec = p.K % V == 0 && aligned16(p.x) && p.ldx % V == 0 && (!p.res || (aligned16(p.res) && p.ldr % V == 0)) &&
                    (!p.h || (aligned16(p.h) && p.ldh % V == 0)) && (!p.w || (aligned16(p.w) && p.ldw % V == 0)) &&
                    aligned(p.codes, V) && p.ldc % V == 0;
-  if (!vec) return launch_rms_v<DT, 1>(p, M, sms, st);
+  if (!vec) {
+    // 5000 x 6001 bf16 with residual: 59 us in shared pieces, 232 element by element
+    const bool flat = p.K >= V && aligned16(p.x) && aligned16(p.res) && aligned16(p.h) && aligned16(p.w) &&
+                      aligned(p.codes, V) && (!p.res || (p.ldr - p.ldx) % V == 0) && (!p.h || (p.ldh - p.ldx) % V == 0) &&
+                      (p.ldc - p.ldx) % V == 0 && (!p.w_rows || p.ldw % V == 0);
+    return flat ? launch_rms_flat<DT>(p, M, sms, st) : launch_rms_v<DT, 1>(p, M, sms, st);
+  }
   const int64_t slot = static_cast<int64_t>(p.K) * (DT == DT_FP32 ? 4 : 2) * (p.res ? 2 : 1);
   // From more than one row an SM on, the ring (4608 x 3072 bf16 with residual:
   // 19.4 us, 22.6 direct; 300 x 3072: 2.9, 3.8 direct; 148 x 3072: 2.4, 2.2 direct)
@@ -183,13 +213,23 @@ svdq_status launch_rope_v(const RopeParams& p, int sms, cudaStream_t st) {
 
 template <int DT>
 svdq_status launch_rope(const RopeParams& p, int sms, cudaStream_t st) {
-  constexpr int V = DT == DT_FP32 ? 4 : 8;
+  // the widest access that every piece of a head starts on (20000 tokens of 20
+  // heads of 70, interleaved: 45 us in 4-byte pieces, 76 element by element)
   const int R = 2 * p.plan.pairs;
-  bool vec = (p.plan.interleaved ? R : R / 2) % V == 0 && (p.plan.D - R) % V == 0;
-  for (const RopeTensor& t : p.t)
-    vec = vec && (t.heads == 0 || (aligned16(t.x) && aligned16(t.out) && t.xb % V == 0 && t.xs % V == 0 &&
-                                   t.xh % V == 0 && t.ob % V == 0 && t.os % V == 0 && t.oh % V == 0));
-  return vec ? launch_rope_v<DT, V>(p, sms, st) : launch_rope_v<DT, 1>(p, sms, st);
+  const int es = DT == DT_FP32 ? 4 : 2;
+  auto fits = [&](int v) {
+    bool ok = (p.plan.interleaved ? R : R / 2) % v == 0 && (p.plan.D - R) % v == 0;
+    for (const RopeTensor& t : p.t)
+      ok = ok && (t.heads == 0 || (aligned(t.x, v * es) && aligned(t.out, v * es) && t.xb % v == 0 && t.xs % v == 0 &&
+                                   t.xh % v == 0 && t.ob % v == 0 && t.os % v == 0 && t.oh % v == 0));
+    return ok;
+  };
+  if constexpr (DT != DT_FP32) {
+    if (fits(8)) return launch_rope_v<DT, 8>(p, sms, st);
+  }
+  if (fits(4)) return launch_rope_v<DT, 4>(p, sms, st);
+  if (fits(2)) return launch_rope_v<DT, 2>(p, sms, st);
+  return launch_rope_v<DT, 1>(p, sms, st);
 }
 
 svdq_status rope_pos(const svdq_rope_positions* pos, RopePos* out) {
