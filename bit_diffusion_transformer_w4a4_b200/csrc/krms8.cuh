@@ -127,8 +127,8 @@ struct RmsParams {
 // Below this the reciprocal top / max|t| would overflow fp32: the row becomes
 // zero codes with a zero scale.
 constexpr float kRmsTiny = 3.0092655e-36f;  // 2^-118
-// The squares of a row with values above about 2^63 overflow fp32: such rows
-// (only those) are summed again scaled by 2^-80.
+// The squares of a row with values above about 2^60 may overflow fp32: such
+// rows (only those) are summed again scaled by 2^-80.
 constexpr float kRmsDown = 8.2718061e-25f;  // 2^-80
 
 // Block-wide sum, in a fixed order; every thread gets it.
@@ -147,31 +147,47 @@ __device__ __forceinline__ float block_sum(float v, float* red, int nw) {
 }
 
 // The row's statistics, joined over the CTA in a fixed order; the barrier
-// also ends the warps' reads of the row.  The maximum is not negative, so its
-// bits are ordered like its values, NaN above infinity.
+// also ends the warps' reads of the row.  Neither is negative, so their bits
+// are ordered like their values, NaN above infinity.  Every thread gets the
+// maximum and whether the sum may be too large for fp32; the sum itself is
+// only joined where it is used, in the first warp.
 struct RmsStats {
   uint64_t ss = 0;   // two partial sums of squares
   float top = 0.f;   // max |t|
 };
-__device__ __forceinline__ void rms8_join(const RmsStats& st, float& ss, uint32_t& top, float* red_s, uint32_t* red_m, int nw) {
-  top = __reduce_max_sync(0xffffffffu, __float_as_uint(st.top));
-  ss = f2_lo(st.ss) + f2_hi(st.ss);
+struct RmsJoined {
+  uint32_t top;
+  float ss;          // first warp
+  bool large;        // a warp's sum is 2^123 or more: with 32 of them the total may overflow
+};
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ RmsJoined rms8_join(const RmsParams& p, const RmsStats& st, float* red_s, uint32_t* red_m, int nw) {
+  constexpr uint32_t kLarge = (123u + 127u) << 23;
+  RmsJoined j;
+  j.top = __reduce_max_sync(0xffffffffu, __float_as_uint(st.top));
+  j.ss = p.norm ? warp_sum(f2_lo(st.ss) + f2_hi(st.ss)) : 0.f;
+  j.large = __float_as_uint(j.ss) >= kLarge;
   if (nw > 1) {
     const int l = threadIdx.x & 31;
     if (l == 0) {
-      red_s[threadIdx.x >> 5] = ss;
-      red_m[threadIdx.x >> 5] = top;
+      red_s[threadIdx.x >> 5] = j.ss;
+      red_m[threadIdx.x >> 5] = j.top;
     }
     __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, l < nw ? red_m[l] : 0u);
-    ss = l < nw ? red_s[l] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    j.top = __reduce_max_sync(0xffffffffu, l < nw ? red_m[l] : 0u);
+    if (p.norm) {
+      const float v = l < nw ? red_s[l] : 0.f;
+      j.large = __reduce_max_sync(0xffffffffu, __float_as_uint(v)) >= kLarge;
+      if (threadIdx.x < 32) j.ss = warp_sum(v);
+    }
   } else {
     __syncwarp();
   }
+  return j;
 }
 
 // t of elements 2i, 2i + 1 (VEC = 1: of the element, with 0).
@@ -220,17 +236,17 @@ __device__ __forceinline__ float rms8_squares_down(const Pack<DT, VEC>& a, float
 // the row's squares summed scaled by kRmsDown (called by the whole CTA or not
 // at all).
 template <class F>
-__device__ __forceinline__ float rms8_scale(const RmsParams& p, int64_t row, float ss, uint32_t top, F again) {
-  const float amax = __uint_as_float(top);
-  const bool finite = top < 0x7F800000u;
+__device__ __forceinline__ float rms8_scale(const RmsParams& p, int64_t row, const RmsJoined& j, F again) {
+  const float amax = __uint_as_float(j.top);
+  const bool finite = j.top < 0x7F800000u;
   const bool live = finite && amax >= kRmsTiny;
   const float lim = p.int8 ? 127.f : 448.f;
   float s2 = 0.f;
-  const bool down = p.norm && finite && !(ss < INFINITY);
+  const bool down = finite && j.large;
   if (down) s2 = again();
   if (threadIdx.x == 0) {
     float rstd = 1.f;
-    if (p.norm) rstd = down ? kRmsDown / sqrtf(s2 * p.inv_K) : 1.f / sqrtf(fmaf(ss, p.inv_K, p.eps));
+    if (p.norm) rstd = down ? kRmsDown / sqrtf(s2 * p.inv_K) : 1.f / sqrtf(fmaf(j.ss, p.inv_K, p.eps));
     p.scales[row] = live ? __fdiv_rn(amax * rstd, lim) : finite ? 0.f : __uint_as_float(0x7FC00000u);
   }
   return live ? __fdiv_rn(lim, amax) : 0.f;
@@ -309,10 +325,8 @@ __global__ void __launch_bounds__(1024, 1) rms8_kernel(const RmsParams p) {
       rms8_stats<DT, VEC, HW>(p, a[c], g, st);
     }
   }
-  float ss;
-  uint32_t top;
-  rms8_join(st, ss, top, red_s, red_m, nw);
-  const float inv = rms8_scale(p, row, ss, top, [&] {
+  const RmsJoined j = rms8_join(p, st, red_s, red_m, nw);
+  const float inv = rms8_scale(p, row, j, [&] {
     float s2 = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -435,10 +449,8 @@ __global__ void __launch_bounds__(512, 1) rms8_flat_kernel(const RmsParams p) {
       rms8_stats<DT, VEC, HW>(p, a[c], g[HW ? c : 0], st);
     }
   }
-  float ss;
-  uint32_t top;
-  rms8_join(st, ss, top, red_s, red_m, nw);
-  const float inv = rms8_scale(p, row, ss, top, [&] {
+  const RmsJoined j = rms8_join(p, st, red_s, red_m, nw);
+  const float inv = rms8_scale(p, row, j, [&] {
     float s2 = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -543,15 +555,13 @@ __global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const
         rms8_stats<DT, VEC, HW>(p, a[c], w[c], st);
       }
     }
-    float ss;
-    uint32_t top;
-    rms8_join(st, ss, top, red_s[it], red_m[it], nw);
+    const RmsJoined j = rms8_join(p, st, red_s[it], red_m[it], nw);
     // every thread has read the slot (the join's barrier): the next row in
     if (threadIdx.x == 0) {
       const int64_t next = row + static_cast<int64_t>(g.slots) * gridDim.x;
       if (next < g.M) issue(next, slot);
     }
-    const float inv = rms8_scale(p, row, ss, top, [&] {
+    const float inv = rms8_scale(p, row, j, [&] {
       float s2 = 0.f;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
