@@ -127,7 +127,10 @@ template <int DT>
 svdq_status launch_rms_flat(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
   constexpr int V = DT == DT_FP32 ? 4 : 8;
   const int64_t pieces = cdiv(p.K + V - 1, V);  // a row may start inside one
-  const int64_t want = M <= 2 * sms ? 1 : pieces <= 256 ? 2 : 4;
+  // pieces a thread: two, which keeps enough rows on an SM (8000 x 4001 fp32:
+  // 85 us, 97 with four), one where that is a few warps (16000 x 701: 33 us, 43
+  // with two) or a few rows have the device to themselves
+  const int64_t want = M <= 2 * sms || (pieces > 64 && pieces <= 128) ? 1 : 2;
   const int64_t ch = std::max(want, cdiv(pieces, 512));
   auto threads = [&](int c) { return static_cast<int>(cdiv(cdiv(pieces, c), 32) * 32); };
   if (ch <= 1) return launch_rms_flat_t<DT, 1>(p, M, threads(1), st);
@@ -189,7 +192,8 @@ svdq_status launch_rms(const RmsParams& p, int64_t M, int sms, cudaStream_t st) 
                    aligned(p.codes, V) && p.ldc % V == 0;
   if (!vec) {
     // 5000 x 6001 bf16 with residual: 59 us in shared pieces, 232 element by element
-    const bool flat = p.K >= V && aligned16(p.x) && aligned16(p.res) && aligned16(p.h) && aligned16(p.w) &&
+    // (and 40 x 101 1.9 us element by element, 3.1 in pieces)
+    const bool flat = p.K >= 32 * V && aligned16(p.x) && aligned16(p.res) && aligned16(p.h) && aligned16(p.w) &&
                       aligned(p.codes, V) && (!p.res || (p.ldr - p.ldx) % V == 0) && (!p.h || (p.ldh - p.ldx) % V == 0) &&
                       (p.ldc - p.ldx) % V == 0 && (!p.w_rows || p.ldw % V == 0);
     return flat ? launch_rms_flat<DT>(p, M, sms, st) : launch_rms_v<DT, 1>(p, M, sms, st);
