@@ -18,6 +18,12 @@
 // 128 bytes of a row (64 16-bit or 128 8-bit elements) in the 128-byte
 // swizzle, and one MMA consumes 32 bytes.  The tensor maps zero-fill rows
 // beyond M and N and elements beyond K.
+//
+// Measured (B200, back to back): bf16 4608 x 3072 -> 3072 with bias, gate and
+// residual 77 us (1.13 PFLOP/s), E4M3 4608 x 3072 -> 12288 with GELU 160 us
+// (2.17), INT8 16896 x 12288 -> 3072 493 us (2.59): all at the power cap, with
+// the tensor pipe busy 72 % of the cycles in the first.  2 x 3072 -> 18432
+// streams its weights at 5.4 TB/s (21 us).
 #pragma once
 
 #include "kg_common.cuh"

@@ -17,7 +17,10 @@
 // all heads of Q and K, so the fp64 work is paid per token and not per head.
 //
 // Bound by memory: every element is read once and written once, in pieces of
-// 16, 8 or 4 bytes as the layout allows (else element by element).
+// 16, 8 or 4 bytes as the layout allows (else element by element).  Groups of
+// four tokens and four CTAs an SM were the fastest of 2, 4, 8 and 3, 4, 5 on
+// 4608 tokens of 48 heads of 128 (bf16, interleaved): 21.5 us, 5.3 TB/s; 32768
+// tokens of 32 heads, split halves: 95 us, 5.7 TB/s.
 #pragma once
 
 #include "krms8.cuh"
