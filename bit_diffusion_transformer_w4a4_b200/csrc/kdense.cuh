@@ -328,8 +328,9 @@ struct DenseTileOut {
 
   // What does not depend on the accumulator, loaded while it is being summed.
   __device__ __forceinline__ void prepare(const DenseParams& p, int n0, int m0, int lane) {
-    const int g0 = p.gate ? m0 / p.gate_rows : 0;
-    one_gate = p.gate && min(m0 + 64, p.M) <= (g0 + 1) * p.gate_rows;
+    const bool gated = p.gate && m0 < p.M;  // tokens beyond M have no gate row
+    const int g0 = gated ? m0 / p.gate_rows : 0;
+    one_gate = gated && min(m0 + 64, p.M) <= (g0 + 1) * p.gate_rows;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const int n = n0 + 8 * f + (lane >> 2);
