@@ -539,8 +539,10 @@ __global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const
       }
     }
     if (!wait_bounded(bar0 + 8 * slot, ph, guard, 0x321)) {
-      if (threadIdx.x == 0)  // the rows on their way land before the CTA leaves
+      if (threadIdx.x == 0) {  // the rows left say so, those on their way land before the CTA leaves
+        for (int64_t left = row; left < g.M; left += gridDim.x) p.scales[left] = __uint_as_float(0x7FC00000u);
         drain_loads(bar0, (1u << g.slots) - 1, ph ? (1u << g.slots) - (1u << slot) : (1u << slot) - 1, g.slots, g.timeout_ns);
+      }
       return;
     }
     const uint8_t* sx = ring + slot * slot_bytes;

@@ -573,7 +573,8 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* desc, void* stream);
  * cancels: they do not depend on the order of any sum.
  * A row whose largest |h weight| is below 2^-118 gets zero codes and the
  * scale 0.  A row that holds a NaN or an infinity, or whose product with the
- * weight overflows fp32, gets the scale NaN; its codes say nothing.
+ * weight overflows fp32, gets the scale NaN; its codes say nothing.  So do
+ * rows that a kernel gave up because a bounded wait expired.
  *   in   SVDQ_BF16, SVDQ_FP16 or SVDQ_FP32: type of x, residual, h, weight
  *   out  SVDQ_E4M3 or SVDQ_INT8
  *   residual [M x K] or NULL; h [M x K] (written) or NULL; h may be x or
