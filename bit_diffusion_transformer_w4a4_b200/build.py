@@ -1,4 +1,5 @@
-"""Build libsvdq.so (the CUDA library behind include/svdq.h) for sm_100a.
+"""Build libsvdq.so (the CUDA library behind include/svdq.h) for sm_100a, and
+_bind.so (the argument marshalling of its tensor operators).
 
 Run ``python -m bit_diffusion_transformer_w4a4_b200.build`` or call
 ``build()``.  The shared object is written next to this file so that it
@@ -12,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvdq.so")
+BIND = os.path.join(HERE, "_bind.so")
 OBJ = os.path.join(HERE, "_build")
 
 NVCC_FLAGS = [
@@ -47,28 +50,56 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _run(cmd: list[str], verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr, file=sys.stderr)
+
+
+def bind_stale() -> bool:
+    if not os.path.exists(BIND):
+        return True
+    t = os.path.getmtime(BIND)
+    return any(os.path.getmtime(s) > t for s in (os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "svdq.h")))
+
+
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """Compile _bind.so against the installed torch (its libraries are loaded
+    by ``import torch``, which comes first)."""
+    if not force and not bind_stale():
+        return BIND
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(ROOT, "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = f"{BIND}.{os.getpid()}.tmp"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *[f"-I{i}" for i in inc], os.path.join(CSRC, "bind.cpp"), "-o", tmp,
+          "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and not stale():
-        return LIB
-    os.makedirs(OBJ, exist_ok=True)
-    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    objs = [os.path.join(OBJ, os.path.basename(u) + ".o") for u in units]
-
-    def run(cmd):
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr, file=sys.stderr)
-
-    inc = ["-I", os.path.join(ROOT, "include")]
+    """Both shared objects; returns the library's path."""
     with concurrent.futures.ThreadPoolExecutor() as ex:
-        list(ex.map(run, ([nvcc(), *NVCC_FLAGS, *(extra or []), *inc, "-c", u, "-o", o]
-                          for u, o in zip(units, objs))))
-    run([nvcc(), *LINK_FLAGS, *objs, "-o", LIB + ".tmp"])
-    os.replace(LIB + ".tmp", LIB)
+        bind = ex.submit(build_bind, force, verbose)
+        if force or stale():
+            os.makedirs(OBJ, exist_ok=True)
+            units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+            objs = [os.path.join(OBJ, os.path.basename(u) + ".o") for u in units]
+            inc = ["-I", os.path.join(ROOT, "include")]
+            list(ex.map(lambda uo: _run([nvcc(), *NVCC_FLAGS, *(extra or []), *inc, "-c", uo[0], "-o", uo[1]], verbose),
+                        zip(units, objs)))
+            _run([nvcc(), *LINK_FLAGS, *objs, "-o", LIB + ".tmp"], verbose)
+            os.replace(LIB + ".tmp", LIB)
+        bind.result()
     return LIB
 
 

@@ -9,7 +9,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 
@@ -366,35 +365,27 @@ def untile_nvfp4_scales(buf: np.ndarray, M: int, K: int) -> np.ndarray:
 # ------------------------------------- operators around the 4-bit layers
 # These take torch tensors whose shapes and strides say what the C structs
 # spell out (2-D tensors with contiguous rows, any row distance).  They run on
-# the tensors' own device, on `stream` or that device's current stream.
+# the tensors' own device, on `stream` or that device's current stream.  Shapes,
+# dtypes and devices are checked in _bind (csrc/bind.cpp), which raises
+# TypeError or ValueError, everything else by the library (SvdqError).
 BF16, FP16, FP32, E4M3, INT8 = range(5)
 ACTS = {None: 0, "none": 0, "gelu": 1, "silu": 2}
+_BIND = None
 
 
-class DenseDesc(ctypes.Structure):
-    _fields_ = [
-        ("in_", ctypes.c_int), ("out", ctypes.c_int), ("act", ctypes.c_int),
-        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
-        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
-        ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
-        ("a_scale", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
-        ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
-        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
-        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
-        ("device_error", ctypes.c_void_p),
-    ]
-
-
-class Rms8Desc(ctypes.Structure):
-    _fields_ = [
-        ("in_", ctypes.c_int), ("out", ctypes.c_int), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
-        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
-        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
-        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
-        ("weight", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("weight_rows", ctypes.c_int64),
-        ("norm", ctypes.c_int), ("eps", ctypes.c_float),
-        ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("scales", ctypes.c_void_p),
-    ]
+def _bind():
+    """The marshalling module (built first when absent or stale)."""
+    global _BIND
+    if _BIND is None:
+        import torch  # noqa: F401  (its libraries have to be loaded)
+        L = lib()
+        if _build.bind_stale():
+            _build.build_bind()
+        from . import _bind as module
+        module.init(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (L.svdq_dense_forward, L.svdq_rms_quantize8, L.svdq_rope_apply)))
+        _BIND = module
+    return _BIND
 
 
 class RopeDesc(ctypes.Structure):
@@ -409,105 +400,6 @@ class RopePositions(ctypes.Structure):
                 ("token_stride", ctypes.c_int64), ("axis_stride", ctypes.c_int64)]
 
 
-class RopeTensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
-                ("stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
-
-
-# The structs again as struct formats: packing one takes a quarter of the time
-# of filling a ctypes.Structure, which a call on a few tokens would feel.
-_DENSE = struct.Struct("@3i4x3q" "Pq" "Pq" "3P" "P2q" "Pq" "Pq" "P")
-_RMS8 = struct.Struct("@2i2q" "Pq" "Pq" "Pq" "P2q" "if" "Pq" "P")
-_ROPE_POS = struct.Struct("@Pi4x3q")
-_ROPE_TENSOR = struct.Struct("@2P7q")
-
-
-class _Torch:
-    """What the calls need of torch, looked up once (importing this module
-    does not import torch)."""
-
-    def __init__(self):
-        import torch
-        self.dtypes = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32,
-                       torch.float8_e4m3fn: E4M3, torch.int8: INT8}
-        self.pos_types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
-        self.f32, self.i32 = torch.float32, torch.int32
-        self.device, self.available = torch.cuda.device, torch.cuda.is_available
-        if self.available():
-            torch.cuda.init()
-            self.current = torch._C._cuda_getDevice
-            self.raw_stream = torch._C._cuda_getCurrentRawStream
-        else:
-            self.current = lambda: None
-
-
-_TORCH = None
-
-
-def _torch() -> _Torch:
-    global _TORCH
-    if _TORCH is None:
-        _TORCH = _Torch()
-    return _TORCH
-
-
-def _dtype(T, t, allowed, what: str) -> int:
-    d = T.dtypes.get(t.dtype)
-    if d not in allowed:
-        raise TypeError(f"{what}: dtype {t.dtype} is not supported here")
-    return d
-
-
-def _differs(t, shape, dtype, what: str):
-    """Raise for the first of t's shape, dtype and device that is not as given."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    raise ValueError(f"{what} is on {t.device}, expected the other tensors' device")
-
-
-def _matrix(t, shape, dtype, dev, what: str) -> int:
-    """Row distance of a matrix with contiguous rows."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
-        _differs(t, shape, dtype, what)
-    ld, step = t.stride()
-    if step != 1 and shape[1] > 1:
-        raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return ld
-
-
-def _vector(t, n, dtype, dev, what: str) -> int:
-    """Address of a contiguous [n] tensor."""
-    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != dev:
-        _differs(t, (n,), dtype, what)
-    if n > 1 and t.stride() != (1,):
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows_of(t, rows_each, M, cols, dtype, dev, what: str):
-    """(row distance, rows each) of a [G x cols] tensor (or [cols]: one row)
-    whose row g serves rows g * rows_each .. of M."""
-    if t.dim() == 1:
-        _vector(t, cols, dtype, dev, what)
-        return cols, max(M, 1)
-    rows_each = int(rows_each) or max(M, 1)
-    if rows_each < 1:
-        raise ValueError(f"{what}: rows each must be positive")
-    return _matrix(t, (-(-M // rows_each), cols), dtype, dev, what), rows_each
-
-
-def _run_on(T, dev: int, stream, call, *args) -> int:
-    """call(*args, stream) where CUDA device `dev` is not the current one."""
-    if dev < 0:
-        if T.available():
-            raise ValueError("the tensors are on the CPU, expected a CUDA device")
-        return call(*args, 0 if stream is None else int(stream))   # the library reports the missing device
-    with T.device(dev):
-        return call(*args, T.raw_stream(dev) if stream is None else int(stream))
-
-
 def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate=None, gate_rows=0,
                   residual=None, device_error=None, stream=None):
     """y = residual + gate * act(a_scale w_scale (a @ w.T) + bias), written to
@@ -518,43 +410,10 @@ def dense_forward(a, w, y, a_scale=None, w_scale=None, bias=None, act=None, gate
     where that is one of them).  a_scale [M] and w_scale [N] are fp32 and for
     8-bit operands only.  act: None, "gelu" (tanh form) or "silu".  gate is [N]
     or [ceil(M / gate_rows), N].  residual may be y."""
-    T = _TORCH or _torch()
-    kind, out = _dtype(T, a, (BF16, FP16, E4M3, INT8), "a"), _dtype(T, y, (BF16, FP16), "y")
-    sa, sw = a.shape, w.shape
-    if len(sa) != 2 or len(sw) != 2:
-        raise ValueError("a and w must be matrices")
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act: {act!r}, expected one of {list(ACTS)}")
-    M, K = sa
-    N = sw[0]
-    dev, it, ot = a.get_device(), a.dtype, y.dtype
-    shape = (M, N)
-    lda, step = a.stride()
-    if step != 1 and K > 1:
-        raise ValueError("a: the elements of a row must be contiguous")
-    ldw, ldy = _matrix(w, (N, K), it, dev, "w"), _matrix(y, shape, ot, dev, "y")
-    sa = sw = pb = pg = pr = pe = ldg = ldr = 0
-    if a_scale is not None:
-        sa = _vector(a_scale, M, T.f32, dev, "a_scale")
-    if w_scale is not None:
-        sw = _vector(w_scale, N, T.f32, dev, "w_scale")
-    if device_error is not None:
-        pe = _vector(device_error, 1, T.i32, dev, "device_error")
-    if bias is not None:
-        pb = _vector(bias, N, ot, dev, "bias")
-    if gate is not None:
-        ldg, gate_rows = _rows_of(gate, gate_rows, M, N, ot, dev, "gate")
-        pg = gate.data_ptr()
-    if residual is not None:
-        ldr = _matrix(residual, shape, ot, dev, "residual")
-        pr = residual.data_ptr()
-    d = _DENSE.pack(kind, out, ACTS[act], M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, sa, sw, pb, pg, ldg, gate_rows,
-                    pr, ldr, y.data_ptr(), ldy, pe)
-    call = (_LIB or lib()).svdq_dense_forward
-    if dev == T.current():
-        code = call(d, T.raw_stream(dev) if stream is None else int(stream))
-    else:
-        code = _run_on(T, dev, stream, call, d)
+    code = (_BIND or _bind()).dense(a, w, y, a_scale, w_scale, bias, code, gate, gate_rows, residual, device_error, stream)
     if code:
         raise SvdqError(code, "svdq_dense_forward")
     return y
@@ -569,35 +428,7 @@ def rms_quantize8(x, codes, scales, residual=None, h=None, weight=None, weight_r
     float8_e4m3fn or int8, scales [M] fp32.  weight is [K] or
     [ceil(M / weight_rows), K].  residual, h and weight may be None; h may be x
     or residual.  Returns (codes, scales)."""
-    T = _TORCH or _torch()
-    kind, out = _dtype(T, x, (BF16, FP16, FP32), "x"), _dtype(T, codes, (E4M3, INT8), "codes")
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError("x must be a matrix")
-    M, K = shape
-    dev, it = x.get_device(), x.dtype
-    ldx, step = x.stride()
-    if step != 1 and K > 1:
-        raise ValueError("x: the elements of a row must be contiguous")
-    ldc = _matrix(codes, shape, codes.dtype, dev, "codes")
-    ps = _vector(scales, M, T.f32, dev, "scales")
-    pr = ph = pw = ldr = ldh = ldw = 0
-    if residual is not None:
-        ldr = _matrix(residual, shape, it, dev, "residual")
-        pr = residual.data_ptr()
-    if h is not None:
-        ldh = _matrix(h, shape, it, dev, "h")
-        ph = h.data_ptr()
-    if weight is not None:
-        ldw, weight_rows = _rows_of(weight, weight_rows, M, K, it, dev, "weight")
-        pw = weight.data_ptr()
-    d = _RMS8.pack(kind, out, M, K, x.data_ptr(), ldx, pr, ldr, ph, ldh, pw, ldw, weight_rows, 1 if norm else 0, eps,
-                   codes.data_ptr(), ldc, ps)
-    call = (_LIB or lib()).svdq_rms_quantize8
-    if dev == T.current():
-        code = call(d, T.raw_stream(dev) if stream is None else int(stream))
-    else:
-        code = _run_on(T, dev, stream, call, d)
+    code = (_BIND or _bind()).rms8(x, codes, scales, residual, h, weight, weight_rows, eps, norm, stream)
     if code:
         raise SvdqError(code, "svdq_rms_quantize8")
     return codes, scales
@@ -624,83 +455,46 @@ class RopeAxes:
         _check(self._lib.svdq_rope_load(ctypes.byref(d), ctypes.byref(h)), "svdq_rope_load")
         self.handle = h
 
-    def _positions(self, T, pos, B, S, dev):
-        """pos [S, axes] (shared by the sequences), [B, S, axes] or [B * S, axes]."""
-        kind = T.pos_types.get(pos.dtype)
-        if kind is None:
-            raise TypeError(f"pos: dtype {pos.dtype} is not supported here")
-        if pos.get_device() != dev:
-            raise ValueError(f"pos is on {pos.device}, expected the other tensors' device")
-        n, shape, st = self.axes, pos.shape, pos.stride()
-        if shape == (B * S, n):
-            return _ROPE_POS.pack(pos.data_ptr(), kind, S * st[0], st[0], st[1])
-        if shape == (S, n):
-            return _ROPE_POS.pack(pos.data_ptr(), kind, 0, st[0], st[1])
-        if shape == (B, S, n):
-            return _ROPE_POS.pack(pos.data_ptr(), kind, *st)
-        raise ValueError(f"pos: shape {tuple(shape)}, expected {(S, n)}, {(B * S, n)} or {(B, S, n)}")
-
-    def _tensor(self, x, out, B, S, dtype, dev, what):
-        shape = x.shape
-        if len(shape) == 4 and shape[0] == B or len(shape) == 3 and B == 1:
-            good = shape[-3] == S and shape[-1] == self.head_dim
-        else:
-            good = False
-        if not good:
-            raise ValueError(f"{what}: shape {tuple(shape)} does not fit {B} sequences of {S} tokens with heads of {self.head_dim}")
-        if x.dtype is not dtype or x.get_device() != dev:
-            _differs(x, shape, dtype, what)
-        if out is None:
-            out = x
-        elif out.shape != shape or out.dtype is not dtype or out.get_device() != dev:
-            _differs(out, shape, dtype, what + "_out")
-        st, so = x.stride(), out.stride()
-        if st[-1] != 1 or so[-1] != 1:
-            raise ValueError(f"{what}: the elements of a head must be contiguous")
-        if len(shape) == 3:
-            st, so = (0, *st), (0, *so)
-        return _ROPE_TENSOR.pack(x.data_ptr(), out.data_ptr(), shape[-2], st[0], st[1], st[2], so[0], so[1], so[2]), out
-
     def apply(self, q, pos, k=None, q_out=None, k_out=None, inverse=False, stream=None):
         """Rotate q and k ([S, H, D] or [B, S, H, D], any strides between heads,
         tokens and sequences; bf16, fp16 or fp32) into q_out and k_out (None: in
         place); ``inverse`` turns back, which is the gradient.  pos is int32,
         int64 or fp32: [S, axes] (shared), [B * S, axes] or [B, S, axes].
         Returns q's output, or both."""
-        T = _TORCH or _torch()
-        kind = _dtype(T, q, (BF16, FP16, FP32), "q")
-        shape = q.shape
-        if len(shape) not in (3, 4):
-            raise ValueError(f"q: shape {tuple(shape)}, expected [(B,) S, H, {self.head_dim}]")
-        B, S = (shape[0] if len(shape) == 4 else 1), shape[-3]
-        dtype, dev, tk = q.dtype, q.get_device(), None
-        tq, q_out = self._tensor(q, q_out, B, S, dtype, dev, "q")
-        if k is not None:
-            tk, k_out = self._tensor(k, k_out, B, S, dtype, dev, "k")
-        p = self._positions(T, pos, B, S, dev)
-        call = self._lib.svdq_rope_apply
-        if dev == T.current():
-            code = call(self.handle, kind, B, S, p, tq, tk, 1 if inverse else 0,
-                        T.raw_stream(dev) if stream is None else int(stream))
-        else:
-            code = _run_on(T, dev, stream, call, self.handle, kind, B, S, p, tq, tk, 1 if inverse else 0)
+        code = (_BIND or _bind()).rope(self.handle.value, self.head_dim, self.axes, q, pos, k, q_out, k_out, inverse, stream)
         if code:
             raise SvdqError(code, "svdq_rope_apply")
-        return q_out if k is None else (q_out, k_out)
+        q_out = q if q_out is None else q_out
+        return q_out if k is None else (q_out, k if k_out is None else k_out)
 
     def table(self, pos, table, stream=None):
         """(cos, sin) of every token and pair into ``table`` (contiguous fp32 of
         tokens x R elements), the ``rope`` argument of ``linear_forward_qkv``
         when R = 128.  pos is [tokens, axes]."""
-        T = _torch()
-        if pos.dim() != 2:
-            raise ValueError(f"pos: shape {tuple(pos.shape)}, expected [tokens, {len(self.axis_dims)}]")
+        import torch
+        types = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
+        if pos.dtype not in types:
+            raise TypeError(f"pos: dtype {pos.dtype} is not supported here")
+        if pos.dim() != 2 or pos.shape[1] != self.axes:
+            raise ValueError(f"pos: shape {tuple(pos.shape)}, expected [tokens, {self.axes}]")
         S = pos.shape[0]
-        if table.dtype != T.f32 or not table.is_contiguous() or table.numel() != S * sum(self.axis_dims):
+        if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() != S * sum(self.axis_dims):
             raise ValueError(f"table: expected {S * sum(self.axis_dims)} contiguous fp32 elements")
-        dev = table.get_device()
-        p = self._positions(T, pos, 1, S, dev)
-        _check(_run_on(T, dev, stream, self._lib.svdq_rope_table, self.handle, 1, S, p, table.data_ptr()), "svdq_rope_table")
+        if table.device != pos.device:
+            raise ValueError(f"table is on {table.device}, expected {pos.device}")
+        p = RopePositions(pos.data_ptr(), types[pos.dtype], 0, *pos.stride())
+
+        def call(s):
+            return self._lib.svdq_rope_table(self.handle, 1, S, ctypes.byref(p), table.data_ptr(), s)
+
+        if pos.is_cuda:
+            with torch.cuda.device(pos.device):
+                code = call(_stream(stream))
+        elif torch.cuda.is_available():
+            raise ValueError(f"the tensors are on {pos.device}, expected a CUDA device")
+        else:
+            code = call(_stream(stream))     # the library reports the missing device
+        _check(code, "svdq_rope_table")
         return table
 
     def close(self) -> None:

