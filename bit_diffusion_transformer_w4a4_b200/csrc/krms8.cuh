@@ -490,7 +490,7 @@ struct RmsRing {
 
 // Shared memory: slots x (x row, residual row), then the barriers.
 template <int DT, int CH, bool HW, bool I8>
-__global__ void __launch_bounds__(512) rms8_ring_kernel(const RmsParams p, const RmsRing g) {
+__global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, const RmsRing g) {
   using E = typename ElemOf<DT>::type;
   constexpr int VEC = 16 / sizeof(E);
   constexpr int SLOTS = 8;
