@@ -241,3 +241,25 @@ def test_rope_python_load_and_table_checks():
     r.close()
     r.close()
 
+
+
+def test_not_tensors_and_bad_numbers():
+    a, w, y = torch.zeros(4, 64, dtype=BF), torch.zeros(8, 64, dtype=BF), torch.zeros(4, 8, dtype=BF)
+    for bad in (dict(a=1), dict(w=None), dict(bias=[1.0]), dict(stream="s"), dict(gate=torch.zeros(1, 8, dtype=BF), gate_rows=1.5)):
+        with pytest.raises(TypeError):
+            svdq.dense_forward(**{**dict(a=a, w=w, y=y), **bad})
+    with pytest.raises(TypeError):
+        svdq.rms_quantize8(a, torch.zeros(4, 64, dtype=torch.int8), None)
+    with pytest.raises(TypeError):
+        svdq.rms_quantize8(a, torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4), eps="x")
+    r = svdq.RopeAxes(64, [32, 32])
+    r.close()
+    with pytest.raises(TypeError):
+        r.apply(torch.zeros(6, 2, 64, dtype=BF), torch.zeros(6, 2, dtype=torch.int32))
+
+
+def test_same_tensor_for_q_and_k_refused():
+    q = torch.zeros(6, 2, 64, dtype=BF)
+    with pytest.raises(svdq.SvdqError) as e:
+        svdq.RopeAxes(64, [32, 32]).apply(q, torch.zeros(6, 2, dtype=torch.int32), k=q)
+    assert e.value.code == ARG
