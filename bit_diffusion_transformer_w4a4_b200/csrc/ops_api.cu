@@ -248,11 +248,12 @@ svdq_status rope_pos(const svdq_rope_positions* pos, RopePos* out) {
 }
 
 // The bytes of a [B, S, H, D] tensor with strides: its dimensions by rising
-// stride, n elements each.
+// stride, n elements each, and as they come.
 struct Nest {
   const void* p;
   int64_t n[3], st[3];  // bytes
   int64_t row;          // bytes of a head
+  int64_t dn[3], dst[3];  // B, S, H (1 and 0 where all heads share one address)
   int64_t span(int dims) const {  // of the `dims` innermost dimensions
     int64_t w = row;
     for (int i = 0; i < dims; ++i) w += (n[i] - 1) * st[i];
@@ -260,7 +261,7 @@ struct Nest {
   }
 };
 Nest nest(const void* p, int64_t B, int64_t S, int64_t H, const int64_t* stride, int64_t D, int es) {
-  Nest t{p, {1, 1, 1}, {0, 0, 0}, D * es};
+  Nest t{p, {1, 1, 1}, {0, 0, 0}, D * es, {1, 1, 1}, {0, 0, 0}};
   const int64_t n[3] = {B, S, H};
   int64_t order[3] = {0, 1, 2};
   std::sort(order, order + 3, [&](int64_t a, int64_t b) {
@@ -269,6 +270,10 @@ Nest nest(const void* p, int64_t B, int64_t S, int64_t H, const int64_t* stride,
   for (int i = 0; i < 3; ++i) {
     t.n[i] = n[order[i]];
     t.st[i] = t.n[i] > 1 ? stride[order[i]] * es : 0;
+    if (n[i] > 1 && stride[i] > 0) {
+      t.dn[i] = n[i];
+      t.dst[i] = stride[i] * es;
+    }
   }
   return t;
 }
@@ -278,15 +283,53 @@ bool nests(const Nest& t) {
     if (t.n[i] > 1 && t.st[i] < t.span(i)) return false;
   return true;
 }
-// Whether two tensors are not known to be apart: neither their spans, nor the
-// column ranges of their outermost dimension, nor (two outermost dimensions
-// that form one) those of the next.
+// Whether heads of two tensors meet whose dimensions have the same strides
+// (those of one entry aside).  Of a dimension only the difference of the two
+// indexes counts, and of that only the few values that bring what is inside
+// the dimension within reach.  Other strides: true.
+struct HeadsMeet {
+  const Nest &a, &b;
+  int64_t st[3];
+  int order[3];  // dimensions by rising stride
+
+  HeadsMeet(const Nest& a_, const Nest& b_) : a(a_), b(b_), order{0, 1, 2} {
+    for (int i = 0; i < 3; ++i) st[i] = std::max(a.dst[i], b.dst[i]);
+    std::sort(order, order + 3, [&](int x, int y) { return st[x] < st[y]; });
+  }
+  int64_t span(const Nest& t, int dims) const {
+    int64_t w = t.row;
+    for (int i = 0; i < dims; ++i) w += (t.dn[order[i]] - 1) * t.dst[order[i]];
+    return w;
+  }
+  // delta: bytes from a's start to b's; dims: the dimensions left
+  bool operator()(int64_t delta, int dims) const {
+    if (delta >= span(a, dims) || -delta >= span(b, dims)) return false;
+    if (dims == 0) return true;
+    const int d = order[dims - 1];
+    if (st[d] == 0) return (*this)(delta, dims - 1);
+    if (a.dn[d] > 1 && b.dn[d] > 1 && a.dst[d] != b.dst[d]) return true;
+    const int64_t in_a = span(a, dims - 1), in_b = span(b, dims - 1);
+    // a's index less b's; the difference from a's entry to b's is delta - e st
+    auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+    const int64_t lo = std::max(floor_div(delta - in_a, st[d]) + 1, 1 - b.dn[d]);
+    const int64_t hi = std::min(floor_div(delta + in_b - 1, st[d]), a.dn[d] - 1);
+    if (hi - lo >= 8) return true;  // heads of one tensor that overlap themselves
+    for (int64_t e = lo; e <= hi; ++e)
+      if ((*this)(delta - e * st[d], dims - 1)) return true;
+    return false;
+  }
+};
+// Whether two tensors are not known to be apart: neither by their spans, nor by
+// the column ranges of their outermost dimension, nor (two outermost dimensions
+// that form one) by those of the next, nor head by head.
 bool may_meet(const Nest& a, const Nest& b) {
   if (!a.p || !b.p) return false;
   if (!overlap(Region{a.p, a.n[2], a.span(2), a.st[2]}, Region{b.p, b.n[2], b.span(2), b.st[2]})) return false;
   auto merges = [](const Nest& t) { return t.n[2] == 1 || t.st[2] == t.n[1] * t.st[1]; };
-  return !merges(a) || !merges(b) ||
-         overlap(Region{a.p, a.n[1] * a.n[2], a.span(1), a.st[1]}, Region{b.p, b.n[1] * b.n[2], b.span(1), b.st[1]});
+  if (merges(a) && merges(b) &&
+      !overlap(Region{a.p, a.n[1] * a.n[2], a.span(1), a.st[1]}, Region{b.p, b.n[1] * b.n[2], b.span(1), b.st[1]}))
+    return false;
+  return HeadsMeet(a, b)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p), 3);
 }
 
 constexpr int64_t kRopeMaxTokens = 1ll << 31;
