@@ -486,7 +486,12 @@ struct RmsRing {
   int slots;       // rows of the ring
   int row_bytes;   // K elements
   uint64_t timeout_ns;
+  int skip_row;    // test hook: the row whose copies are left out (-1: none)
 };
+
+// In place of a warp's maximum of |t|: the warp has given the row up.  Above
+// every maximum, NaN included.
+constexpr uint32_t kRmsGivenUp = 0xFFFFFFFFu;
 
 // Shared memory: slots x (x row, residual row), then the barriers.
 template <int DT, int CH, bool HW, bool I8>
@@ -514,6 +519,7 @@ __global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, co
   auto issue = [&](int64_t row, int slot) {  // thread 0
     const uint32_t dst = smem_u32(ring) + slot * slot_bytes;
     mbar_expect_tx(bar0 + 8 * slot, slot_bytes);
+    if (row == g.skip_row) return;
     bulk_load(dst, static_cast<const E*>(p.x) + row * p.ldx, g.row_bytes, bar0 + 8 * slot);
     if (p.res) bulk_load(dst + g.row_bytes, static_cast<const E*>(p.res) + row * p.ldr, g.row_bytes, bar0 + 8 * slot);
   };
@@ -527,7 +533,8 @@ __global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, co
   int slot = 0;
   uint32_t ph = 0;
   int it = 0;
-  for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x, it ^= 1) {
+  int64_t row = blockIdx.x;
+  for (; row < g.M; row += gridDim.x, it ^= 1) {
     if (HW && row >= w_end) {
       const int64_t w_row = p.w_rows ? row / p.w_rows : 0;
       w_end = p.w_rows ? (w_row + 1) * p.w_rows : g.M;
@@ -538,12 +545,13 @@ __global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, co
         if (k < p.K) w[c].load_cached(src + k);
       }
     }
-    if (!wait_bounded(bar0 + 8 * slot, ph, guard, 0x321)) {
-      if (threadIdx.x == 0) {  // the rows left say so, those on their way land before the CTA leaves
-        for (int64_t left = row; left < g.M; left += gridDim.x) p.scales[left] = __uint_as_float(0x7FC00000u);
-        drain_loads(bar0, (1u << g.slots) - 1, ph ? (1u << g.slots) - (1u << slot) : (1u << slot) - 1, g.slots, g.timeout_ns);
+    // a warp with an expired wait says so at the join's barrier: the CTA goes on or gives up as one
+    if (!__all_sync(0xffffffffu, wait_bounded(bar0 + 8 * slot, ph, guard, 0x321))) {
+      if (nw > 1) {
+        if ((threadIdx.x & 31) == 0) red_m[it][threadIdx.x >> 5] = kRmsGivenUp;
+        __syncthreads();
       }
-      return;
+      break;
     }
     const uint8_t* sx = ring + slot * slot_bytes;
     Pack<DT, VEC> a[CH];
@@ -563,6 +571,7 @@ __global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, co
       }
     }
     const RmsJoined j = rms8_join(p, st, red_s[it], red_m[it], nw);
+    if (j.top == kRmsGivenUp) break;
     // every thread has read the slot (the join's barrier): the next row in
     if (threadIdx.x == 0) {
       const int64_t next = row + static_cast<int64_t>(g.slots) * gridDim.x;
@@ -583,6 +592,10 @@ __global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, co
       if (k < p.K) rms8_codes<DT, VEC, HW, I8>(a[c], w[c], inv, p.codes + row * p.ldc + k);
     }
     if (++slot == g.slots) { slot = 0; ph ^= 1; }
+  }
+  if (row < g.M && threadIdx.x == 0) {  // given up: the rows left say so, copies on their way land before the CTA leaves
+    for (int64_t left = row; left < g.M; left += gridDim.x) p.scales[left] = __uint_as_float(0x7FC00000u);
+    drain_loads(bar0, (1u << g.slots) - 1, ph ? (1u << g.slots) - (1u << slot) : (1u << slot) - 1, g.slots, g.timeout_ns);
   }
 }
 

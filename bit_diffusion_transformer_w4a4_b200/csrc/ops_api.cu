@@ -45,6 +45,14 @@ svdq_status device_info(DeviceInfo* d) {
   return SVDQ_OK;
 }
 
+// svdq_ops_debug_set_fault of this thread.
+struct OpsDebug {
+  uint32_t mask = 0;
+  uint64_t timeout_ns = kDefaultTimeoutNs;
+};
+thread_local OpsDebug ops_debug;
+constexpr uint32_t kFaultDense = 1, kFaultNorm = 2;
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int dtype_size(int t) { return t == SVDQ_FP32 ? 4 : t == SVDQ_BF16 || t == SVDQ_FP16 ? 2 : 1; }
 
@@ -160,7 +168,7 @@ svdq_status launch_rms_ring_k(const RmsParams& p, int64_t M, int sms, int nt, cu
   const int smem = kRmsSlots * slot;
   const int by_regs = 65536 / (static_cast<int>(cdiv(regs, 8) * 8) * nt);
   const int per_sm = std::max(1, std::min({(227 * 1024) / (smem + 2048), by_regs, 2048 / nt, 32}));
-  RmsRing g{M, kRmsSlots, row_bytes, kDefaultTimeoutNs};
+  RmsRing g{M, kRmsSlots, row_bytes, ops_debug.timeout_ns, ops_debug.mask & kFaultNorm ? static_cast<int>(M / 3) : -1};
   LaunchCfg lc(dim3(static_cast<unsigned>(std::min<int64_t>(M, static_cast<int64_t>(sms) * per_sm))), dim3(nt), smem, st);
   SVDQ_TRY(cudaLaunchKernelEx(&lc.cfg, rms8_ring_kernel<DT, CH, HW, I8>, p, g));
   return SVDQ_OK;
@@ -609,6 +617,13 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
   if (d->in == SVDQ_BF16) return launch_rms<DT_BF16>(p, M, dev.sms, st);
   if (d->in == SVDQ_FP16) return launch_rms<DT_FP16>(p, M, dev.sms, st);
   return launch_rms<DT_FP32>(p, M, dev.sms, st);
+}
+
+svdq_status svdq_ops_debug_set_fault(uint32_t mask, uint32_t timeout_us) {
+  if (mask & ~(kFaultDense | kFaultNorm)) return SVDQ_ERR_INVALID_ARG;
+  ops_debug.mask = mask;
+  ops_debug.timeout_ns = timeout_us ? static_cast<uint64_t>(timeout_us) * 1000ull : kDefaultTimeoutNs;
+  return SVDQ_OK;
 }
 
 svdq_status svdq_rope_load(const svdq_rope_desc* d, svdq_rope_t* out) {

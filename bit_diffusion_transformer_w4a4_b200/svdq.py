@@ -39,7 +39,7 @@ EXPORTED = [
     "svdq_w4a4_gemm_lowrank_up_chain", "svdq_linear_forward_chain", "svdq_device_error_site",
     "svdq_set_deterministic",
     "svdq_dense_forward", "svdq_rms_quantize8",
-    "svdq_rope_load", "svdq_rope_free", "svdq_rope_apply", "svdq_rope_table",
+    "svdq_rope_load", "svdq_rope_free", "svdq_rope_apply", "svdq_rope_table", "svdq_ops_debug_set_fault",
 ]
 
 
@@ -112,6 +112,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.svdq_quantize_act_lowrank_down_static.argtypes = [st, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.svdq_dense_forward.argtypes = [vp, vp]
     L.svdq_rms_quantize8.argtypes = [vp, vp]
+    L.svdq_ops_debug_set_fault.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
     L.svdq_rope_load.argtypes = [vp, ctypes.POINTER(vp)]
     L.svdq_rope_free.argtypes = [vp]
     L.svdq_rope_apply.argtypes = [vp, st, i64, i64, vp, vp, vp, st, vp]
@@ -432,6 +433,10 @@ def rms_quantize8(x, codes, scales, residual=None, h=None, weight=None, weight_r
     if code:
         raise SvdqError(code, "svdq_rms_quantize8")
     return codes, scales
+
+
+def ops_debug_set_fault(mask: int, timeout_us: int) -> None:
+    _check(lib().svdq_ops_debug_set_fault(mask, timeout_us), "svdq_ops_debug_set_fault")
 
 
 class RopeAxes:

@@ -605,6 +605,15 @@ typedef struct {
 svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream);
 
 /*
+ * Test hook: calls of svdq_rms_quantize8 that the calling thread makes from
+ * now on leave out the copies of row M / 3 (mask bit 1; only the form for many
+ * 16-byte aligned rows copies rows) and use `timeout_us` as the bounded-wait
+ * limit (0 restores the default of 2 s).  The wait for it then expires; no GPU
+ * fault is involved.
+ */
+svdq_status svdq_ops_debug_set_fault(uint32_t mask, uint32_t timeout_us);
+
+/*
  * Rotary positions with several axes (text index, time, height, width, ...).
  * A head's first R = sum axis_dim elements rotate in R/2 pairs: the first
  * axis_dim[0] / 2 pairs by the token's position on axis 0, the next by axis
