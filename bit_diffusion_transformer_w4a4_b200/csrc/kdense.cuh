@@ -56,6 +56,7 @@ struct DenseParams {
   int store;              // form of the stores and residual loads (below)
   int* err;               // or null
   uint64_t timeout_ns;
+  int stuck;              // test hook: the first CTA's first stage waits for an arrival that never comes
 };
 
 __device__ int g_dense_err;  // error word of calls that pass none
@@ -244,10 +245,19 @@ __device__ __forceinline__ void dense_store(const DenseParams& p, const DenseLan
   }
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+// Sets the abort flag (at `flag` of each CTA's shared memory) of all CTAs of
+// the cluster.  A thread that has given up calls it before a cluster barrier,
+// behind which the cluster's CTAs then agree.
+__device__ __forceinline__ void raise_in_cluster(uint32_t flag, int ctas) {
+  for (int r = 0; r < ctas; ++r) st_cluster_u32(mapa_shared(flag, r), 1);
 }
 // The sums over `split` CTAs (ranks step o + first) of a feature's NC
 // consecutive tokens at `addr` of each one's [token][128 features] partial
@@ -444,6 +454,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 5);
   const uint32_t bar_res = smem_u32(bars + 2 * NST + 6);        // one per pair of epilogue warps
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // the stages that this CTA has loaded and the parities of their last loads
+  volatile uint32_t* loads = reinterpret_cast<volatile uint32_t*>(bars + 2 * NST + 6 + DP_EPI_WARPS / 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -456,13 +468,12 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblk) * pr / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblk) * (pr + 1) / split);
   const uint16_t both = static_cast<uint16_t>(0x3u << lead);
-  bool good = true;
   const Guard guard{p.err ? p.err : &g_dense_err, abort_flag, p.timeout_ns};
   const int num_tiles = p.num_f * p.num_t;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 1 + (p.stuck && s + blockIdx.x == 0));
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -500,7 +511,6 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         const int arow = tt * BN + static_cast<int>(rank) * (BN / 2);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait_bounded(bar_empty + 8 * s, ph ^ 1, guard, 0x301))) break;
-          issued &= ~(1u << s);
           const uint32_t st = sbase + s * S::STAGE;
           if (rank == 0) mbar_expect_tx(bar_full + 8 * s, S::TX);
           // whole boxes always: what lies beyond N, M or K is zero-filled
@@ -512,7 +522,8 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
           if (++s == NST) { s = 0; ph ^= 1; }
         }
       }
-      if (*abort_flag && rank == 0) drain_loads(bar_full, issued, issued_par, NST, p.timeout_ns);
+      loads[0] = issued;
+      loads[1] = issued_par;
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -605,8 +616,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
         continue;
       }
       if (split > 1) {  // one tile per cluster: the partial sums take the stages' place
-        good = __all_sync(0xffffffffu, wait_bounded(bar_acc_full, 0, guard, 0x304, 64));
-        if (!good) break;
+        if (!__all_sync(0xffffffffu, wait_bounded(bar_acc_full, 0, guard, 0x304, 64))) break;
         tc_fence_after();
         uint32_t* part = reinterpret_cast<uint32_t*>(smem);
 #pragma unroll 1
@@ -671,11 +681,13 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
     }
   }
 
+  __syncwarp();
+  if (*abort_flag) raise_in_cluster(smem_u32(const_cast<int*>(abort_flag)), 2 * split);
   if constexpr (!TILED) {
     if (split > 1) {
       __syncwarp();
-      cluster_sync();  // every pair's partial sums are in place
-      if (warp >= 4 && good) {
+      cluster_sync();  // every pair's partial sums are in place, or all know that some are not
+      if (warp >= 4 && !*abort_flag) {
         const int e = warp - 4, q = warp & 3;
         int ft, tt;
         dense_tile(p, cid, ft, tt);
@@ -709,6 +721,16 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // the pair's MMAs, loads and remote arrivals are all done
+  // Given up (every CTA of the cluster knows): loads on their way land before a
+  // CTA leaves.  The leader's barriers count those of both; a stage that only
+  // the other CTA has loaded was loaded a wait's limit ago.  Passing that CTA's
+  // stages on as well takes registers from the epilogue (INT8 16896 x 12288 ->
+  // 3072 499 -> 505 us).
+  if (*abort_flag) {
+    if (threadIdx.x == 0 && rank == 0) drain_loads(bar_full, loads[0], loads[1], NST, p.timeout_ns);
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -753,6 +775,8 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
   const uint32_t bar_drain = smem_u32(bars + 2 * NST + 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // the stages that this CTA has loaded and the parities of their last loads
+  volatile uint32_t* loads = reinterpret_cast<volatile uint32_t*>(bars + 2 * NST + 3);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -766,7 +790,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 1 + (p.stuck && s + blockIdx.x == 0));
       mbar_init(bar_empty + 8 * s, 1);
     }
     mbar_init(bar_acc, 1);
@@ -793,7 +817,6 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
       uint32_t ph = 0, issued = 0, issued_par = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_bounded(bar_empty + 8 * s, ph ^ 1, guard, 0x311)) break;
-        issued &= ~(1u << s);
         const uint32_t st = sbase + s * S::STAGE;
         mbar_expect_tx(bar_full + 8 * s, S::STAGE);
         const int kc = kb * (KIND == DK_F16 ? 64 : 128);
@@ -803,7 +826,8 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
         issued_par = (issued_par & ~(1u << s)) | (ph << s);
         if (++s == NST) { s = 0; ph ^= 1; }
       }
-      if (*abort_flag) drain_loads(bar_full, issued, issued_par, NST, p.timeout_ns);
+      loads[0] = issued;
+      loads[1] = issued_par;
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -881,8 +905,10 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
   }
   __syncwarp();
   if (split > 1) {
-    cluster_sync();  // all partial tiles are in place
-    if (warp >= 2 && ok) {
+    cluster_sync();  // all partial tiles are in place, or their CTAs' flags are up
+    if (warp >= 2) {
+      // asked under the first loads of the partial tiles
+      const uint32_t lost = lane < split ? ld_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), lane)) : 0u;
       // this CTA's tokens: 16 at a time where there are as many, else two
       const int unit = valid >= 16 * split ? 16 : 2;
       const int per = unit * ((valid + unit * split - 1) / (unit * split));
@@ -898,6 +924,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
             else dense_residual<OUT, 16, false>(p, l, m0 + c, n, r);
           }
           dense_join<KIND, 16>(sbase + (c * 128 + f) * 4, split, 1, 0, v);
+          if (__any_sync(0xffffffffu, lost)) break;
           dense_math<KIND, OUT, 16>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
           if (p.store == STORE_PAIRED) dense_store<OUT, 16, true>(p, l, m0 + c, n, x, r);
           else dense_store<OUT, 16, false>(p, l, m0 + c, n, x, r);
@@ -908,6 +935,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
           uint64_t x[1];
           if (p.res) dense_residual<OUT, 2, false>(p, l, m0 + c, n, r);
           dense_join<KIND, 2>(sbase + (c * 128 + f) * 4, split, 1, 0, v);
+          if (__any_sync(0xffffffffu, lost)) break;
           dense_math<KIND, OUT, 2>(p, l, m0 + c, n, v, sc ? sc + c : nullptr, x);
           dense_store<OUT, 2, false>(p, l, m0 + c, n, x, r);
         }
@@ -917,6 +945,8 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
   }
   tc_fence_before();
   __syncthreads();
+  // given up: loads still on their way land before the CTA leaves
+  if (threadIdx.x == 0 && *abort_flag) drain_loads(bar_full, loads[0], loads[1], NST, p.timeout_ns);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, COLS);

@@ -559,7 +559,8 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
   // that its map gives it: N itself a multiple of them too
   c.tiled = M > 1 && N % 8 == 0 && rows_by(8) && (!d->residual || d->ldr > 0);
   c.p.err = d->device_error;
-  c.p.timeout_ns = kDefaultTimeoutNs;
+  c.p.timeout_ns = ops_debug.timeout_ns;
+  c.p.stuck = (ops_debug.mask & kFaultDense) != 0;
   const bool bf = d->out == SVDQ_BF16;
   if (wide) return bf ? launch_dense<DK_F16, DT_BF16>(c) : launch_dense<DK_F16, DT_FP16>(c);
   if (d->in == SVDQ_E4M3) return bf ? launch_dense<DK_E4M3, DT_BF16>(c) : launch_dense<DK_E4M3, DT_FP16>(c);
@@ -622,7 +623,7 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
 svdq_status svdq_ops_debug_set_fault(uint32_t mask, uint32_t timeout_us) {
   if (mask & ~(kFaultDense | kFaultNorm)) return SVDQ_ERR_INVALID_ARG;
   ops_debug.mask = mask;
-  ops_debug.timeout_ns = timeout_us ? static_cast<uint64_t>(timeout_us) * 1000ull : kDefaultTimeoutNs;
+  ops_debug.timeout_ns = timeout_us ? std::max<uint64_t>(timeout_us, 1000) * 1000ull : kDefaultTimeoutNs;
   return SVDQ_OK;
 }
 

@@ -605,11 +605,12 @@ typedef struct {
 svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream);
 
 /*
- * Test hook: calls of svdq_rms_quantize8 that the calling thread makes from
- * now on leave out the copies of row M / 3 (mask bit 1; only the form for many
- * 16-byte aligned rows copies rows) and use `timeout_us` as the bounded-wait
- * limit (0 restores the default of 2 s).  The wait for it then expires; no GPU
- * fault is involved.
+ * Test hook: in the calls that the calling thread makes from now on a wait
+ * runs out (mask bit 0: svdq_dense_forward, a stage of the first tile counts
+ * an arrival too many; bit 1: svdq_rms_quantize8 in its form for many 16-byte
+ * aligned rows, which copies rows, leaves out the copies of row M / 3), and
+ * `timeout_us` is the limit of bounded waits (at least 1000; 0 restores the
+ * default of 2 s).  No GPU fault is involved.
  */
 svdq_status svdq_ops_debug_set_fault(uint32_t mask, uint32_t timeout_us);
 

@@ -1,6 +1,6 @@
-"""Bounded waits of the operators that expire: the test hook leaves copies out
-and shortens the limit, so that a wait runs out; the kernels end, what they did
-not compute is marked or left as it was, and everything else is right."""
+"""Bounded waits of the norm that expire: the test hook leaves a row's copies out
+and shortens the limit; the kernel ends, the rows that it gave up are marked,
+and all others are right."""
 import pytest
 
 from bit_diffusion_transformer_w4a4_b200 import svdq
