@@ -59,8 +59,6 @@ struct DenseParams {
   int stuck;              // test hook: the first CTA's first stage waits for an arrival that never comes
 };
 
-__device__ int g_dense_err;  // error word of calls that pass none
-
 __host__ __device__ constexpr uint32_t idesc_dense(int kind, int out, int M, int N) {
   // D format f32 / s32; operand format bf16 (1) or fp16 (0), E4M3 (0), S8 (1)
   const uint32_t d = kind == DK_INT8 ? 2u : 1u;
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(DP_THREADS, 1)
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblk) * pr / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblk) * (pr + 1) / split);
   const uint16_t both = static_cast<uint16_t>(0x3u << lead);
-  const Guard guard{p.err ? p.err : &g_dense_err, abort_flag, p.timeout_ns};
+  const Guard guard{p.err ? p.err : &g_ops_err, abort_flag, p.timeout_ns};
   const int num_tiles = p.num_f * p.num_t;
 
   if (threadIdx.x == 0) {
@@ -786,7 +784,7 @@ __global__ void __launch_bounds__(DS_THREADS, 2)
   const int ft = tile % p.num_f, tt = tile / p.num_f;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblk) * rank / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblk) * (rank + 1) / split);
-  const Guard guard{p.err ? p.err : &g_dense_err, abort_flag, p.timeout_ns};
+  const Guard guard{p.err ? p.err : &g_ops_err, abort_flag, p.timeout_ns};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {

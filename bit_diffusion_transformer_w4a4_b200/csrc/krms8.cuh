@@ -479,7 +479,9 @@ __global__ void __launch_bounds__(512, 1) rms8_flat_kernel(const RmsParams p) {
 }
 
 // ------------------------------------------------------------- the ring form
-__device__ int g_rms8_err;  // error word of the bounded waits (this call reports none)
+// Wait site of the first bounded wait that expired in a call without an error
+// word of its own; svdq_ops_device_error_site reads and clears it.
+__device__ int g_ops_err;
 
 struct RmsRing {
   int64_t M;
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(512, 2) rms8_ring_kernel(const RmsParams p, co
   __shared__ int abort_flag;
   const int nt = blockDim.x, nw = nt >> 5;
   const uint32_t bar0 = smem_u32(bars);
-  const Guard guard{&g_rms8_err, &abort_flag, g.timeout_ns};
+  const Guard guard{&g_ops_err, &abort_flag, g.timeout_ns};
   const uint32_t slot_bytes = g.row_bytes * (p.res ? 2u : 1u);
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.slots; ++i) mbar_init(bar0 + 8 * i, 1);

@@ -620,6 +620,26 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
   return launch_rms<DT_FP32>(p, M, dev.sms, st);
 }
 
+svdq_status svdq_ops_device_error_site(void* stream, int* site) {
+  if (!site) return SVDQ_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (svdq_status s = device_info(&dev); s != SVDQ_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capturing;
+  SVDQ_TRY(cudaStreamIsCapturing(st, &capturing));
+  if (capturing != cudaStreamCaptureStatusNone) return SVDQ_ERR_INVALID_ARG;
+  int seen = 0;
+  SVDQ_TRY(cudaMemcpyFromSymbolAsync(&seen, g_ops_err, sizeof(int), 0, cudaMemcpyDeviceToHost, st));
+  SVDQ_TRY(cudaStreamSynchronize(st));
+  if (seen) {
+    const int none = 0;
+    SVDQ_TRY(cudaMemcpyToSymbolAsync(g_ops_err, &none, sizeof(int), 0, cudaMemcpyHostToDevice, st));
+    SVDQ_TRY(cudaStreamSynchronize(st));
+  }
+  *site = seen;
+  return SVDQ_OK;
+}
+
 svdq_status svdq_ops_debug_set_fault(uint32_t mask, uint32_t timeout_us) {
   if (mask & ~(kFaultDense | kFaultNorm)) return SVDQ_ERR_INVALID_ARG;
   ops_debug.mask = mask;

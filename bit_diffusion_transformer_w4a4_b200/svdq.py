@@ -39,7 +39,8 @@ EXPORTED = [
     "svdq_w4a4_gemm_lowrank_up_chain", "svdq_linear_forward_chain", "svdq_device_error_site",
     "svdq_set_deterministic",
     "svdq_dense_forward", "svdq_rms_quantize8",
-    "svdq_rope_load", "svdq_rope_free", "svdq_rope_apply", "svdq_rope_table", "svdq_ops_debug_set_fault",
+    "svdq_rope_load", "svdq_rope_free", "svdq_rope_apply", "svdq_rope_table", "svdq_ops_device_error_site",
+    "svdq_ops_debug_set_fault",
 ]
 
 
@@ -112,6 +113,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.svdq_quantize_act_lowrank_down_static.argtypes = [st, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     L.svdq_dense_forward.argtypes = [vp, vp]
     L.svdq_rms_quantize8.argtypes = [vp, vp]
+    L.svdq_ops_device_error_site.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     L.svdq_ops_debug_set_fault.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
     L.svdq_rope_load.argtypes = [vp, ctypes.POINTER(vp)]
     L.svdq_rope_free.argtypes = [vp]
@@ -433,6 +435,15 @@ def rms_quantize8(x, codes, scales, residual=None, h=None, weight=None, weight_r
     if code:
         raise SvdqError(code, "svdq_rms_quantize8")
     return codes, scales
+
+
+def ops_error_site(stream=None) -> int:
+    """Wait-site code of the first bounded wait that expired on the current
+    device since the last ask (0 if none), in rms_quantize8 or in dense_forward
+    without device_error; clears it.  Synchronises the stream."""
+    v = ctypes.c_int(0)
+    _check(lib().svdq_ops_device_error_site(_stream(stream), ctypes.byref(v)), "svdq_ops_device_error_site")
+    return int(v.value)
 
 
 def ops_debug_set_fault(mask: int, timeout_us: int) -> None:

@@ -534,8 +534,9 @@ typedef enum {
  *   residual [M x N]; ldr = 0 adds one row to every token; may be y itself
  *        (same pointer and row distance)
  *   device_error device int, set to a nonzero wait-site code if a bounded
- *        wait expires (never cleared by the library); may be NULL, such a
- *        failure then is reported to no one
+ *        wait expires (never cleared by the library); where it is NULL,
+ *        svdq_ops_device_error_site reports it.  Elements of y whose sum such
+ *        a call did not finish are left as they were
  * 0 <= M <= 2^24, 1 <= N <= 2^24, 1 <= K <= 65536, and at most 2^27 tiles of
  * 16 tokens by 128 features.  Rows beyond M are left as they were.
  */
@@ -574,7 +575,8 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* desc, void* stream);
  * A row whose largest |h weight| is below 2^-118 gets zero codes and the
  * scale 0.  A row that holds a NaN or an infinity, or whose product with the
  * weight overflows fp32, gets the scale NaN; its codes say nothing.  So do
- * rows that a kernel gave up because a bounded wait expired.
+ * rows that a kernel gave up because a bounded wait expired, which
+ * svdq_ops_device_error_site reports.
  *   in   SVDQ_BF16, SVDQ_FP16 or SVDQ_FP32: type of x, residual, h, weight
  *   out  SVDQ_E4M3 or SVDQ_INT8
  *   residual [M x K] or NULL; h [M x K] (written) or NULL; h may be x or
@@ -603,6 +605,15 @@ typedef struct {
   float* scales;
 } svdq_rms8_desc;
 svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream);
+
+/*
+ * Failure reporting: synchronise `stream` and write to *site the wait-site
+ * code of the first bounded wait that expired on the current device since the
+ * last ask (0: none), in a call of svdq_rms_quantize8 or of
+ * svdq_dense_forward without device_error, clearing it.  `stream` must not be
+ * capturing (SVDQ_ERR_INVALID_ARG).
+ */
+svdq_status svdq_ops_device_error_site(void* stream, int* site);
 
 /*
  * Test hook: in the calls that the calling thread makes from now on a wait
