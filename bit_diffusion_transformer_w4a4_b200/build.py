@@ -1,14 +1,18 @@
 """Build libsvdq.so (the CUDA library behind include/svdq.h) for sm_100a, and
 _bind.so (the argument marshalling of its tensor operators).
 
-Run ``python -m bit_diffusion_transformer_w4a4_b200.build`` or call
-``build()``.  The shared object is written next to this file so that it
-travels with the source tree; it is rebuilt when any source is newer.
+``build()`` compiles the library, which needs nvcc alone; ``build_bind()`` the
+marshalling, which needs the installed torch and a C++ compiler (the first call
+of a tensor operator runs it).  ``python -m
+bit_diffusion_transformer_w4a4_b200.build`` does both, the second where torch is
+installed.  The shared objects are written next to this file so that they
+travel with the source tree; they are rebuilt when any source is newer.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -87,19 +91,18 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Both shared objects; returns the library's path."""
+    """The library; returns its path."""
+    if not force and not stale():
+        return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    objs = [os.path.join(OBJ, os.path.basename(u) + ".o") for u in units]
+    inc = ["-I", os.path.join(ROOT, "include")]
     with concurrent.futures.ThreadPoolExecutor() as ex:
-        bind = ex.submit(build_bind, force, verbose)
-        if force or stale():
-            os.makedirs(OBJ, exist_ok=True)
-            units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-            objs = [os.path.join(OBJ, os.path.basename(u) + ".o") for u in units]
-            inc = ["-I", os.path.join(ROOT, "include")]
-            list(ex.map(lambda uo: _run([nvcc(), *NVCC_FLAGS, *(extra or []), *inc, "-c", uo[0], "-o", uo[1]], verbose),
-                        zip(units, objs)))
-            _run([nvcc(), *LINK_FLAGS, *objs, "-o", LIB + ".tmp"], verbose)
-            os.replace(LIB + ".tmp", LIB)
-        bind.result()
+        list(ex.map(lambda uo: _run([nvcc(), *NVCC_FLAGS, *(extra or []), *inc, "-c", uo[0], "-o", uo[1]], verbose),
+                    zip(units, objs)))
+    _run([nvcc(), *LINK_FLAGS, *objs, "-o", LIB + ".tmp"], verbose)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 
@@ -107,3 +110,5 @@ if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else None)
     print(LIB)
+    if importlib.util.find_spec("torch"):
+        print(build_bind(force="--force" in sys.argv, verbose=True))
