@@ -1,5 +1,5 @@
 """Build libsvdq.so (the CUDA library behind include/svdq.h) for sm_100a, and
-_bind.so (the argument marshalling of its tensor operators).
+_bind.*.so (the argument marshalling of its tensor operators).
 
 ``build()`` compiles the library, which needs nvcc alone; ``build_bind()`` the
 marshalling, which needs the installed torch and a C++ compiler (the first call
@@ -14,6 +14,7 @@ import concurrent.futures
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -23,7 +24,6 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvdq.so")
-BIND = os.path.join(HERE, "_bind.so")
 OBJ = os.path.join(HERE, "_build")
 
 NVCC_FLAGS = [
@@ -64,30 +64,41 @@ def _run(cmd: list[str], verbose: bool) -> None:
         print(r.stdout + r.stderr, file=sys.stderr)
 
 
+def bind_path() -> str:
+    """The marshalling module of this interpreter and the installed torch: it
+    uses torch's C++ interface, which changes from build to build, so each has
+    a file of its own."""
+    import torch
+    tag = f"{sys.implementation.cache_tag}-torch{torch.__version__}-{(torch.version.git_version or '')[:8]}"
+    return os.path.join(HERE, f"_bind.{re.sub('[^0-9A-Za-z.-]', '_', tag)}.so")
+
+
 def bind_stale() -> bool:
-    if not os.path.exists(BIND):
+    path = bind_path()
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(BIND)
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(s) > t for s in (os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "svdq.h")))
 
 
 def build_bind(force: bool = False, verbose: bool = False) -> str:
-    """Compile _bind.so against the installed torch (its libraries are loaded
-    by ``import torch``, which comes first)."""
+    """Compile the marshalling against the installed torch (its libraries are
+    loaded by ``import torch``, which comes first)."""
+    path = bind_path()
     if not force and not bind_stale():
-        return BIND
+        return path
     import torch
     from torch.utils.cpp_extension import include_paths
     inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(ROOT, "include"),
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
-    tmp = f"{BIND}.{os.getpid()}.tmp"
+    tmp = f"{path}.{os.getpid()}.tmp"
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *[f"-I{i}" for i in inc], os.path.join(CSRC, "bind.cpp"), "-o", tmp,
           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
-    os.replace(tmp, BIND)
-    return BIND
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

@@ -8,6 +8,7 @@ library is missing or the device is not an sm_100 GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -382,9 +383,9 @@ def _bind():
     if _BIND is None:
         import torch  # noqa: F401  (its libraries have to be loaded)
         L = lib()
-        if _build.bind_stale():
-            _build.build_bind()
-        from . import _bind as module
+        spec = importlib.util.spec_from_file_location(f"{__package__}._bind", _build.build_bind())
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
         module.init(*(ctypes.cast(f, ctypes.c_void_p).value
                       for f in (L.svdq_dense_forward, L.svdq_rms_quantize8, L.svdq_rope_apply)))
         _BIND = module

@@ -1,7 +1,13 @@
-"""What building and loading needs: the C ABI nothing but nvcc."""
+"""What building and loading needs: the C ABI nothing but nvcc, the tensor
+operators' module the torch that it is compiled against."""
 import os
 import subprocess
 import sys
+
+import pytest
+import torch
+
+from bit_diffusion_transformer_w4a4_b200 import build, svdq
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -20,3 +26,11 @@ print(svdq.lib().svdq_version().decode())
                        capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr
     assert "sm_100a" in r.stdout
+
+
+@pytest.mark.parametrize("version", ["2.11.1", "0.0.0+other"])
+def test_module_of_another_torch_is_not_loaded(monkeypatch, version):
+    svdq._bind()
+    assert not build.bind_stale()
+    monkeypatch.setattr(torch, "__version__", version)
+    assert build.bind_stale()
