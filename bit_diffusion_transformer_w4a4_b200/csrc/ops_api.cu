@@ -495,8 +495,10 @@ svdq_status launch_dense(DenseCall& c) {
 
 extern "C" {
 
-svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
-  if (!d) return SVDQ_ERR_INVALID_ARG;
+svdq_status svdq_dense_forward(const svdq_dense_desc* desc, void* stream) {
+  if (!desc) return SVDQ_ERR_INVALID_ARG;
+  svdq_dense_desc own = *desc;
+  const svdq_dense_desc* d = &own;
   const bool wide = d->in == SVDQ_BF16 || d->in == SVDQ_FP16;
   if (!wide && d->in != SVDQ_E4M3 && d->in != SVDQ_INT8) return SVDQ_ERR_INVALID_ARG;
   if (d->out != SVDQ_BF16 && d->out != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
@@ -508,10 +510,17 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
   if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 24) || K < 1 || K > 65536) return SVDQ_ERR_SHAPE;
   if (cdiv(M, 16) * cdiv(N, 128) > (1 << 27)) return SVDQ_ERR_SHAPE;
   constexpr int64_t kLdMax = 1ll << 36;
+  if ((d->residual && d->ldr < 0) || (d->gate && (d->gate_rows < 1 || d->ldg < 0))) return SVDQ_ERR_SHAPE;
+  // the distance of a single row says nothing
+  if (M <= 1) {
+    own.lda = K;
+    own.ldy = own.ldr = N;
+  }
+  if (N == 1) own.ldw = K;
+  if (d->gate && d->gate_rows >= M) own.ldg = N;
   if ((M > 1 && (d->lda < K || d->ldy < N)) || (N > 1 && d->ldw < K)) return SVDQ_ERR_SHAPE;
   if (d->lda > kLdMax || d->ldw > kLdMax || d->ldy > kLdMax) return SVDQ_ERR_SHAPE;
-  if (d->residual && (d->ldr < 0 || d->ldr > kLdMax)) return SVDQ_ERR_SHAPE;
-  if (d->gate && (d->gate_rows < 1 || d->ldg < 0 || d->ldg > kLdMax)) return SVDQ_ERR_SHAPE;
+  if ((d->residual && d->ldr > kLdMax) || (d->gate && d->ldg > kLdMax)) return SVDQ_ERR_SHAPE;
   if (M == 0) return SVDQ_OK;
   if (!d->a || !d->w || !d->y) return SVDQ_ERR_INVALID_ARG;
   // rows that are read through tensor maps start on 16-byte boundaries
@@ -567,8 +576,10 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* d, void* stream) {
   return bf ? launch_dense<DK_INT8, DT_BF16>(c) : launch_dense<DK_INT8, DT_FP16>(c);
 }
 
-svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
-  if (!d) return SVDQ_ERR_INVALID_ARG;
+svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream) {
+  if (!desc) return SVDQ_ERR_INVALID_ARG;
+  svdq_rms8_desc own = *desc;
+  const svdq_rms8_desc* d = &own;
   if (d->in != SVDQ_BF16 && d->in != SVDQ_FP16 && d->in != SVDQ_FP32) return SVDQ_ERR_INVALID_ARG;
   if (d->out != SVDQ_E4M3 && d->out != SVDQ_INT8) return SVDQ_ERR_INVALID_ARG;
   if (d->norm != 0 && d->norm != 1) return SVDQ_ERR_INVALID_ARG;
@@ -576,10 +587,14 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* d, void* stream) {
   const int64_t M = d->M, K = d->K;
   if (M < 0 || M > INT32_MAX || K < 1 || K > 32768) return SVDQ_ERR_SHAPE;
   constexpr int64_t kLdMax = 1ll << 28;
-  if (d->ldx < 0 || d->ldx > kLdMax || (d->residual && (d->ldr < 0 || d->ldr > kLdMax))) return SVDQ_ERR_SHAPE;
+  if (d->ldx < 0 || (d->residual && d->ldr < 0) || (d->weight && (d->weight_rows < 1 || d->ldw < 0))) return SVDQ_ERR_SHAPE;
+  // the distance of a single row says nothing
+  if (M <= 1) own.ldx = own.ldr = own.ldh = own.ldc = K;
+  if (d->weight && d->weight_rows >= M) own.ldw = K;
+  if (d->ldx > kLdMax || (d->residual && d->ldr > kLdMax)) return SVDQ_ERR_SHAPE;
   if (M > 1 && (d->ldc < K || (d->h && d->ldh < K))) return SVDQ_ERR_SHAPE;
   if (d->ldc > kLdMax || (d->h && d->ldh > kLdMax)) return SVDQ_ERR_SHAPE;
-  if (d->weight && (d->weight_rows < 1 || d->ldw < 0 || d->ldw > kLdMax)) return SVDQ_ERR_SHAPE;
+  if (d->weight && d->ldw > kLdMax) return SVDQ_ERR_SHAPE;
   if (M == 0) return SVDQ_OK;
   if (!d->x || !d->codes || !d->scales) return SVDQ_ERR_INVALID_ARG;
   const int es = dtype_size(d->in);

@@ -496,8 +496,9 @@ svdq_status svdq_selftest_division(int variant, unsigned long long* mismatches);
  * captured graphs too) and run on the current device, whose memory the
  * buffers must be.  Outputs must not overlap inputs except where a call says
  * so; overlaps that the host can see return SVDQ_ERR_INVALID_ARG.  Row
- * distances (ld*) are in elements; that of a single row is not looked at.  A
- * call for no rows (M = 0, B or S = 0) returns SVDQ_OK and does nothing.
+ * distances (ld*) are in elements and not negative; that of a single row says
+ * nothing.  A call for no rows (M = 0, B or S = 0) returns SVDQ_OK and does
+ * nothing.
  */
 typedef enum {
   SVDQ_BF16 = 0,
