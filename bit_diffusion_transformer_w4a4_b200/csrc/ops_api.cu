@@ -244,17 +244,6 @@ svdq_status launch_rope(const RopeParams& p, int sms, cudaStream_t st) {
   return launch_rope_v<DT, 1>(p, sms, st);
 }
 
-svdq_status rope_pos(const svdq_rope_positions* pos, RopePos* out) {
-  if (!pos) return SVDQ_ERR_INVALID_ARG;
-  if (pos->type != SVDQ_POS_INT32 && pos->type != SVDQ_POS_INT64 && pos->type != SVDQ_POS_FP32)
-    return SVDQ_ERR_INVALID_ARG;
-  if (!pos->p) return SVDQ_ERR_INVALID_ARG;
-  if (!aligned(pos->p, pos->type == SVDQ_POS_INT64 ? 8 : 4)) return SVDQ_ERR_ALIGNMENT;
-  if (pos->batch_stride < 0 || pos->token_stride < 0 || pos->axis_stride < 0) return SVDQ_ERR_SHAPE;
-  *out = RopePos{pos->p, static_cast<int>(pos->type), pos->batch_stride, pos->token_stride, pos->axis_stride};
-  return SVDQ_OK;
-}
-
 // The bytes of a [B, S, H, D] tensor with strides: its dimensions by rising
 // stride, n elements each, and as they come.
 struct Nest {
@@ -342,6 +331,20 @@ bool may_meet(const Nest& a, const Nest& b) {
 
 constexpr int64_t kRopeMaxTokens = 1ll << 31;
 constexpr int64_t kRopeMaxSpan = 1ll << 44;  // elements of a dimension's extent
+
+svdq_status rope_pos(const svdq_rope_positions* pos, int64_t B, int64_t S, int axes, RopePos* out, Nest* where) {
+  if (!pos) return SVDQ_ERR_INVALID_ARG;
+  if (pos->type != SVDQ_POS_INT32 && pos->type != SVDQ_POS_INT64 && pos->type != SVDQ_POS_FP32)
+    return SVDQ_ERR_INVALID_ARG;
+  if (!pos->p) return SVDQ_ERR_INVALID_ARG;
+  if (!aligned(pos->p, pos->type == SVDQ_POS_INT64 ? 8 : 4)) return SVDQ_ERR_ALIGNMENT;
+  const int64_t stride[3] = {pos->batch_stride, pos->token_stride, pos->axis_stride}, n[3] = {B, S, axes};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] < 0 || (n[i] > 1 && stride[i] > kRopeMaxSpan / n[i])) return SVDQ_ERR_SHAPE;
+  *where = nest(pos->p, B, S, axes, stride, 1, pos->type == SVDQ_POS_INT64 ? 8 : 4);
+  *out = RopePos{pos->p, static_cast<int>(pos->type), pos->batch_stride, pos->token_stride, pos->axis_stride};
+  return SVDQ_OK;
+}
 
 // ---------------------------------------------------------------------- dense
 // Clusters of two CTAs that fit on the device at once (cached per device,
@@ -537,6 +540,10 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* desc, void* stream) {
       overlap(y, Region{d->a_scale, 1, 4 * M, 4 * M}) || overlap(y, Region{d->w_scale, 1, 4 * N, 4 * N}) ||
       (overlap(y, r) && !same(y, r)))
     return SVDQ_ERR_INVALID_ARG;
+  for (const Region& t : {y, Region{d->a, M, K * es, d->lda * es}, Region{d->w, N, K * es, d->ldw * es},
+                          Region{d->bias, 1, 2 * N, 2 * N}, Region{d->gate, gates, 2 * N, 2 * d->ldg}, r,
+                          Region{d->a_scale, 1, 4 * M, 4 * M}, Region{d->w_scale, 1, 4 * N, 4 * N}})
+    if (overlap(t, Region{d->device_error, 1, 4, t.ld})) return SVDQ_ERR_INVALID_ARG;
   DenseCall c;
   c.d = d;
   if (svdq_status s = device_info(&c.dev); s != SVDQ_OK) return s;
@@ -733,7 +740,9 @@ svdq_status svdq_rope_apply(svdq_rope_t h, svdq_dtype dtype, int64_t B, int64_t 
   }
   if (may_meet(to[0], to[1]) || may_meet(to[0], from[1]) || may_meet(from[0], to[1])) return SVDQ_ERR_INVALID_ARG;
   if (B == 0 || S == 0 || p.t[0].heads + p.t[1].heads == 0) return SVDQ_OK;
-  if (svdq_status s = rope_pos(pos, &p.pos); s != SVDQ_OK) return s;
+  Nest at;
+  if (svdq_status s = rope_pos(pos, B, S, h->axes, &p.pos, &at); s != SVDQ_OK) return s;
+  if (may_meet(at, to[0]) || may_meet(at, to[1])) return SVDQ_ERR_INVALID_ARG;
   DeviceInfo dev;
   if (svdq_status s = device_info(&dev); s != SVDQ_OK) return s;
   p.plan = h->plan;
@@ -755,7 +764,10 @@ svdq_status svdq_rope_table(svdq_rope_t h, int64_t B, int64_t S, const svdq_rope
   if (!table) return SVDQ_ERR_INVALID_ARG;
   if (!aligned(table, 8)) return SVDQ_ERR_ALIGNMENT;
   RopeTableParams p{};
-  if (svdq_status s = rope_pos(pos, &p.pos); s != SVDQ_OK) return s;
+  Nest at;
+  if (svdq_status s = rope_pos(pos, B, S, h->axes, &p.pos, &at); s != SVDQ_OK) return s;
+  const int64_t bytes = B * S * h->plan.pairs * 8;
+  if (overlap(Region{at.p, 1, at.span(3), 0}, Region{table, 1, bytes, 0})) return SVDQ_ERR_INVALID_ARG;
   DeviceInfo dev;
   if (svdq_status s = device_info(&dev); s != SVDQ_OK) return s;
   p.plan = h->plan;

@@ -27,3 +27,41 @@ def test_dense_distance_of_a_single_row(kw, code):
 ])
 def test_norm_distance_of_a_single_row(kw, code):
     assert _rms(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(device_error=Y), ARG), (dict(device_error=Y + 2 * 200 * 99 + 396), ARG), (dict(device_error=A + 16), ARG),
+    (dict(device_error=W), ARG), (dict(device_error=B, bias=B), ARG), (dict(device_error=G + 4, gate=G), ARG),
+    (dict(device_error=R, residual=R), ARG), (dict(device_error=SA, in_=svdq.E4M3, a_scale=SA, w_scale=SW), ARG),
+    (dict(device_error=SW + 4, in_=svdq.E4M3, a_scale=SA, w_scale=SW), ARG),
+    (dict(device_error=Y + 2 * 200 * 100), DEVICE), (dict(device_error=Y + 400, ldy=202), DEVICE),
+])
+def test_dense_error_word_is_an_output(kw, code):
+    assert _dense(**kw) == code
+
+
+def _positions(at, B=2, S=10, **pos):
+    """svdq_rope_apply of X in place with its positions at `at`."""
+    from test_ops_cpu import _rope_apply
+    return _rope_apply(B=B, S=S, q=dict(out=X), pos={**dict(p=at), **pos})
+
+
+@pytest.mark.parametrize("at,pos,code", [
+    (X, {}, ARG), (X + 2 * 3840 - 4, {}, ARG), (X + 2 * 3840, {}, DEVICE), (X - 40 * 4, {}, DEVICE), (X - 40 * 4 + 4, {}, ARG),
+    (X - 40 * 8 + 8, dict(type=1), ARG), (X - 40 * 8, dict(type=1), DEVICE), (X - 8, dict(batch_stride=0, token_stride=0), DEVICE),
+    (X - 4, dict(batch_stride=0, token_stride=0), ARG), (0x7000000, dict(token_stride=1 << 60), SHAPE),
+])
+def test_positions_are_not_in_an_output(at, pos, code):
+    assert _positions(at, **pos) == code
+
+
+def test_table_is_not_in_the_positions():
+    import ctypes
+    L = svdq.lib()
+    h = ctypes.c_void_p(0)
+    desc = svdq.RopeDesc(64, 2, (32, 32, 0, 0), (1e4, 1e4, 0, 0), 1, 0)
+    assert L.svdq_rope_load(ctypes.byref(desc), ctypes.byref(h)) == 0
+    p = svdq.RopePositions(X, 0, 0, 2, 1)
+    for at, code in ((X, ARG), (X + 72, ARG), (X + 80, DEVICE), (X - 8 * 32 * 10, DEVICE), (X - 8 * 32 * 10 + 8, ARG)):
+        assert L.svdq_rope_table(h, 1, 10, ctypes.byref(p), at, None) == code, hex(at)
+    L.svdq_rope_free(h)
