@@ -532,7 +532,7 @@ svdq_status svdq_dense_forward(const svdq_dense_desc* desc, void* stream) {
   if (!aligned(d->y, 2) || !aligned(d->bias, 2) || !aligned(d->gate, 2) || !aligned(d->residual, 2) ||
       !aligned(d->a_scale, 4) || !aligned(d->w_scale, 4) || !aligned(d->device_error, 4))
     return SVDQ_ERR_ALIGNMENT;
-  const int64_t gates = d->gate ? cdiv(M, d->gate_rows) : 0;
+  const int64_t gates = d->gate ? (M - 1) / d->gate_rows + 1 : 0;
   const Region y{d->y, M, 2 * N, 2 * d->ldy};
   const Region r{d->residual, M, 2 * N, 2 * d->ldr};
   if (overlap(y, Region{d->a, M, K * es, d->lda * es}) || overlap(y, Region{d->w, N, K * es, d->ldw * es}) ||
@@ -611,7 +611,7 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream) {
   const Region x{d->x, M, K * es, d->ldx * es}, r{d->residual, M, K * es, d->ldr * es};
   const Region h{d->h, M, K * es, d->ldh * es}, c{d->codes, M, K, d->ldc};
   const Region s{d->scales, 1, 4 * M, 4 * M};
-  const Region w{d->weight, d->weight ? cdiv(M, d->weight_rows) : 0, K * es, d->ldw * es};
+  const Region w{d->weight, d->weight ? (M - 1) / d->weight_rows + 1 : 0, K * es, d->ldw * es};
   if ((overlap(h, x) && !same(h, x)) || (overlap(h, r) && !same(h, r)) || overlap(h, w) || overlap(h, c) ||
       overlap(h, s) || overlap(c, x) || overlap(c, r) || overlap(c, w) || overlap(c, s) || overlap(s, x) ||
       overlap(s, r) || overlap(s, w))

@@ -65,3 +65,24 @@ def test_table_is_not_in_the_positions():
     for at, code in ((X, ARG), (X + 72, ARG), (X + 80, DEVICE), (X - 8 * 32 * 10, DEVICE), (X - 8 * 32 * 10 + 8, ARG)):
         assert L.svdq_rope_table(h, 1, 10, ctypes.byref(p), at, None) == code, hex(at)
     L.svdq_rope_free(h)
+
+
+MOST = (1 << 63) - 1
+
+
+@pytest.mark.parametrize("rows", [100, MOST - 50, MOST])
+def test_rows_each_at_its_largest(rows):
+    """ceil(M / rows) must not overflow: the one row's overlap is still seen."""
+    assert _dense(gate=G, gate_rows=rows) == DEVICE
+    assert _dense(gate=Y, gate_rows=rows) == ARG
+    assert _rms(weight=WT, weight_rows=rows) == DEVICE
+    assert _rms(weight=C, weight_rows=rows) == ARG
+
+
+def test_rows_each_at_its_largest_in_python():
+    a, w, y = torch.zeros(4, 64, dtype=BF), torch.zeros(8, 64, dtype=BF), torch.zeros(4, 8, dtype=BF)
+    for rows in (4, MOST - 1, MOST):
+        with pytest.raises(svdq.SvdqError):
+            svdq.dense_forward(a, w, y, gate=torch.zeros(1, 8, dtype=BF), gate_rows=rows)
+        with pytest.raises(ValueError):
+            svdq.dense_forward(a, w, y, gate=torch.zeros(2, 8, dtype=BF), gate_rows=rows)
