@@ -46,6 +46,12 @@ int64_t integer(PyObject* o, const char* what) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+
 int device_of(const at::Tensor& t) { return t.is_cuda() ? t.get_device() : -1; }
 
 int dtype_of(const at::Tensor& t) {
@@ -218,7 +224,7 @@ PyObject* rms8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const double eps = PyFloat_AsDouble(v[7]);
     if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
     d.eps = static_cast<float>(eps);
-    d.norm = PyObject_IsTrue(v[8]) == 1;
+    d.norm = truth(v[8]);
     return run(dev, v[9], [&](void* s) { return g_rms8(&d, s); });
   });
 }
@@ -279,7 +285,7 @@ PyObject* rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
     } else {
       raise(PyExc_ValueError, "pos: expected [S, axes], [B * S, axes] or [B, S, axes]");
     }
-    const int inverse = PyObject_IsTrue(v[8]) == 1;
+    const int inverse = truth(v[8]);
     return run(dev, v[9], [&](void* s) {
       return g_rope(h, type, B, S, &p, &tq, v[5] == Py_None ? nullptr : &tk, inverse, s);
     });

@@ -86,3 +86,17 @@ def test_rows_each_at_its_largest_in_python():
             svdq.dense_forward(a, w, y, gate=torch.zeros(1, 8, dtype=BF), gate_rows=rows)
         with pytest.raises(ValueError):
             svdq.dense_forward(a, w, y, gate=torch.zeros(2, 8, dtype=BF), gate_rows=rows)
+
+
+class NoTruth:
+    def __bool__(self):
+        raise KeyError("no truth value")
+
+
+def test_flag_without_a_truth_value():
+    """The object's own exception, not a SystemError."""
+    x, codes, scales = torch.zeros(4, 64, dtype=BF), torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    with pytest.raises(KeyError):
+        svdq.rms_quantize8(x, codes, scales, norm=NoTruth())
+    with pytest.raises(KeyError):
+        svdq.RopeAxes(64, [32, 32]).apply(torch.zeros(6, 2, 64, dtype=BF), torch.zeros(6, 2, dtype=torch.int32), inverse=NoTruth())
