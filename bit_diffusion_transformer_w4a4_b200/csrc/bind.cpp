@@ -107,7 +107,8 @@ const void* rows_of(PyObject* o, int64_t M, int64_t cols, at::ScalarType type, i
   }
   if (*each == 0) *each = M > 0 ? M : 1;
   if (*each < 1) raise(PyExc_ValueError, "%s: rows each must be positive", what);
-  *ld = matrix(t, M > 0 ? (M - 1) / *each + 1 : 0, cols, type, dev, what);
+  // rows of no tokens: as many as there are
+  *ld = matrix(t, M > 0 ? (M - 1) / *each + 1 : t.dim() == 2 ? t.size(0) : 0, cols, type, dev, what);
   return t.data_ptr();
 }
 

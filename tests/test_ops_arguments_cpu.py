@@ -100,3 +100,15 @@ def test_flag_without_a_truth_value():
         svdq.rms_quantize8(x, codes, scales, norm=NoTruth())
     with pytest.raises(KeyError):
         svdq.RopeAxes(64, [32, 32]).apply(torch.zeros(6, 2, 64, dtype=BF), torch.zeros(6, 2, dtype=torch.int32), inverse=NoTruth())
+
+
+@pytest.mark.parametrize("rows", [0, 1, 50])
+def test_no_tokens_with_the_gates_and_weights_of_some_images(rows):
+    """A call for no rows does nothing, whatever rows its gate or weight has."""
+    w, y = torch.zeros(8, 64, dtype=BF), torch.zeros(0, 8, dtype=BF)
+    for n in (0, 1, 2):
+        assert svdq.dense_forward(torch.zeros(0, 64, dtype=BF), w, y, gate=torch.zeros(n, 8, dtype=BF), gate_rows=rows) is y
+        svdq.rms_quantize8(torch.zeros(0, 64, dtype=BF), torch.zeros(0, 64, dtype=torch.int8), torch.zeros(0),
+                           weight=torch.zeros(n, 64, dtype=BF), weight_rows=rows)
+    with pytest.raises(ValueError):
+        svdq.dense_forward(torch.zeros(0, 64, dtype=BF), w, y, gate=torch.zeros(2, 9, dtype=BF), gate_rows=rows)
