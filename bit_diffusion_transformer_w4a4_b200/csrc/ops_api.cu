@@ -662,6 +662,17 @@ svdq_status svdq_ops_device_error_site(void* stream, int* site) {
   return SVDQ_OK;
 }
 
+svdq_status svdq_ops_debug_dense_variant(int64_t M, int64_t N, int64_t K, svdq_dtype in, int sms, int* variant) {
+  if (!variant || sms < 1) return SVDQ_ERR_INVALID_ARG;
+  if (in != SVDQ_BF16 && in != SVDQ_FP16 && in != SVDQ_E4M3 && in != SVDQ_INT8) return SVDQ_ERR_INVALID_ARG;
+  if (M < 1 || M > (1 << 24) || N < 1 || N > (1 << 24) || K < 1 || K > 65536) return SVDQ_ERR_SHAPE;
+  const DenseChoice v = dense_choose(M, N, static_cast<int>(cdiv(K * dtype_size(in), 128)), sms);
+  variant[0] = v.pair;
+  variant[1] = v.bn;
+  variant[2] = v.split;
+  return SVDQ_OK;
+}
+
 svdq_status svdq_ops_debug_set_fault(uint32_t mask, uint32_t timeout_us) {
   if (mask & ~(kFaultDense | kFaultNorm)) return SVDQ_ERR_INVALID_ARG;
   ops_debug.mask = mask;

@@ -41,7 +41,7 @@ EXPORTED = [
     "svdq_set_deterministic",
     "svdq_dense_forward", "svdq_rms_quantize8",
     "svdq_rope_load", "svdq_rope_free", "svdq_rope_apply", "svdq_rope_table", "svdq_ops_device_error_site",
-    "svdq_ops_debug_set_fault",
+    "svdq_ops_debug_set_fault", "svdq_ops_debug_dense_variant",
 ]
 
 
@@ -115,6 +115,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.svdq_dense_forward.argtypes = [vp, vp]
     L.svdq_rms_quantize8.argtypes = [vp, vp]
     L.svdq_ops_device_error_site.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+    L.svdq_ops_debug_dense_variant.argtypes = [i64, i64, i64, st, ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     L.svdq_ops_debug_set_fault.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
     L.svdq_rope_load.argtypes = [vp, ctypes.POINTER(vp)]
     L.svdq_rope_free.argtypes = [vp]
@@ -445,6 +446,13 @@ def ops_error_site(stream=None) -> int:
     v = ctypes.c_int(0)
     _check(lib().svdq_ops_device_error_site(_stream(stream), ctypes.byref(v)), "svdq_ops_device_error_site")
     return int(v.value)
+
+
+def ops_debug_dense_variant(M: int, N: int, K: int, in_: int, sms: int) -> tuple:
+    """(pair of SMs, tokens per tile, K split) of dense_forward on this shape."""
+    v = (ctypes.c_int * 3)()
+    _check(lib().svdq_ops_debug_dense_variant(M, N, K, in_, sms, v), "svdq_ops_debug_dense_variant")
+    return tuple(v)
 
 
 def ops_debug_set_fault(mask: int, timeout_us: int) -> None:

@@ -617,6 +617,13 @@ svdq_status svdq_rms_quantize8(const svdq_rms8_desc* desc, void* stream);
 svdq_status svdq_ops_device_error_site(void* stream, int* site);
 
 /*
+ * Test hook: the kernel that svdq_dense_forward takes for a shape on a device
+ * of `sms` SMs: whether pairs of SMs share a tile, tokens per tile, and CTAs
+ * (pairs) that share a tile's K range.  Host arithmetic only.
+ */
+svdq_status svdq_ops_debug_dense_variant(int64_t M, int64_t N, int64_t K, svdq_dtype in, int sms, int* variant);
+
+/*
  * Test hook: in the calls that the calling thread makes from now on a wait
  * runs out (mask bit 0: svdq_dense_forward, a stage of the first tile counts
  * an arrival too many; bit 1: svdq_rms_quantize8 in its form for many 16-byte
