@@ -20,10 +20,13 @@
 // beyond M and N and elements beyond K.
 //
 // Measured (B200, back to back): bf16 4608 x 3072 -> 3072 with bias, gate and
-// residual 77 us (1.13 PFLOP/s), E4M3 4608 x 3072 -> 12288 with GELU 160 us
-// (2.17), INT8 16896 x 12288 -> 3072 493 us (2.59): all at the power cap, with
-// the tensor pipe busy 72 % of the cycles in the first.  2 x 3072 -> 18432
-// streams its weights at 5.4 TB/s (21 us).
+// residual 77 us (1.13 PFLOP/s), E4M3 4608 x 3072 -> 12288 with GELU 163 us
+// (2.14), INT8 16896 x 12288 -> 3072 496 us (2.57); on different boxes 75 to
+// 78, 158 to 169 and 484 to 518.  All three draw 984 to 993 of the 1000 W, at
+// 1462, 1342 and 1290 MHz; the tensor pipe is busy 72 and 74 % of the cycles in
+// the first two, L2 41 and 42 %.  2 x 3072 -> 18432 streams its weights at
+// 5.3 TB/s (21 us).  A gate row per token, read element by element, costs the
+// first call 31 us (77 -> 108).
 #pragma once
 
 #include "kg_common.cuh"

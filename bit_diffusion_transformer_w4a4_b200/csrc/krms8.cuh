@@ -26,9 +26,10 @@
 //                     memory (bulk copies), so that loads do not pause while
 //                     a row is reduced and converted
 //
-// Measured (B200): bf16 4608 x 3072 with residual and weight 19.6 us (99 MB,
-// 5.1 TB/s), 16896 x 12288 without either 100 us (623 MB, 6.2 TB/s), one row
-// of 4096 2.2 us, packed rows of 5000 x 6001 with residual and weight 61 us
+// Measured (B200): bf16 4608 x 3072 with residual and weight 19.9 us (99 MB,
+// 5.0 TB/s; with a weight row for every row 25.7), 16896 x 12288 without either
+// 101 us (623 MB, 6.2 TB/s), fp32 4608 x 3072 33.6 us (184 MB, 5.5 TB/s), one
+// row of 4096 2.2 us, packed rows of 5000 x 6001 with residual and weight 61 us
 // (210 MB, 3.4 TB/s).
 #pragma once
 

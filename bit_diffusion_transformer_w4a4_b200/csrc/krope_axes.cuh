@@ -20,7 +20,9 @@
 // 16, 8 or 4 bytes as the layout allows (else element by element).  Groups of
 // four tokens and four CTAs an SM were the fastest of 2, 4, 8 and 3, 4, 5 on
 // 4608 tokens of 48 heads of 128 (bf16, interleaved): 21.5 us, 5.3 TB/s; 32768
-// tokens of 32 heads, split halves: 95 us, 5.7 TB/s.
+// tokens of 32 heads, split halves: 95 us, 5.6 TB/s.  Heads that only allow
+// narrow pieces pay for it: 20000 tokens of 20 heads of 70 take 45 us
+// interleaved (4 bytes) and 51 us in split halves (2 bytes), floor 17.
 #pragma once
 
 #include "krms8.cuh"
@@ -201,7 +203,10 @@ struct RopeTableParams {
   float2* table;                 // [tokens][pairs]
 };
 
-// One thread per table entry; bound by the 8-byte stores.
+// One thread per table entry.  Far from the memory's speed (4608 tokens of 64
+// pairs 5.8 us, 16896 18.0 us: 0.4 us and 1.4 us of stores): the lanes' own
+// indexes into the parameters replay, and every entry pays two 64-bit
+// divisions, the fp64 reduction and the sincospi.
 __global__ void __launch_bounds__(ROPE_THREADS) rope_table_kernel(const __grid_constant__ RopeTableParams p) {
   griddep_wait();
   griddep_launch_dependents();

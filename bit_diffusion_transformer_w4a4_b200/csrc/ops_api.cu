@@ -135,9 +135,13 @@ template <int DT>
 svdq_status launch_rms_flat(const RmsParams& p, int64_t M, int sms, cudaStream_t st) {
   constexpr int V = DT == DT_FP32 ? 4 : 8;
   const int64_t pieces = cdiv(p.K + V - 1, V);  // a row may start inside one
-  // pieces a thread: two, which keeps enough rows on an SM (8000 x 4001 fp32:
-  // 85 us, 97 with four), one where that is a few warps (16000 x 701: 33 us, 43
-  // with two) or a few rows have the device to themselves
+  // pieces a thread: two (8000 x 4001 fp32 85 us, 97 with four; bf16 16000 x 301
+  // 22.8, 27.3 with one; 8000 x 2047 36.7, 40.9 with one), but one
+  //   where a few rows have the device to themselves (296 x 2047 bf16 3.4 us, 3.9
+  //   with two; the other way 296 x 4001, 4.6 and 4.3), and
+  //   for 65 to 128 pieces, which two a thread spread over two warps of 33 to 64
+  //   threads (16000 x 701 33.5 us, 42.9 with two; 2000 x 851 7.0, 7.9; the other
+  //   way from about 97 pieces on with many rows: 16000 x 901 40.2 and 36.1)
   const int64_t want = M <= 2 * sms || (pieces > 64 && pieces <= 128) ? 1 : 2;
   const int64_t ch = std::max(want, cdiv(pieces, 512));
   auto threads = [&](int c) { return static_cast<int>(cdiv(cdiv(pieces, c), 32) * 32); };

@@ -490,15 +490,15 @@ svdq_status svdq_selftest_division(int variant, unsigned long long* mismatches);
  * Operators around the 4-bit layers of a transformer block: layers kept at 16
  * or 8 bits, the norm in front of an 8-bit layer, and rotary positions.  No
  * counterpart on the pages (their runtime leaves these to the host
- * framework); they let a block whose linears are this library's run without
- * one.  The calls take every buffer from the caller, allocate nothing, keep
- * nothing between calls (calls may overlap freely, on any streams, in
- * captured graphs too) and run on the current device, whose memory the
- * buffers must be.  Outputs must not overlap inputs except where a call says
- * so; overlaps that the host can see return SVDQ_ERR_INVALID_ARG.  Row
- * distances (ld*) are in elements and not negative; that of a single row says
- * nothing.  A call for no rows (M = 0, B or S = 0) returns SVDQ_OK and does
- * nothing.
+ * framework).  A block still needs attention, and models whose norm subtracts
+ * a mean or takes a shift (adaLN) that norm, from elsewhere.  The calls take
+ * every buffer from the caller, allocate nothing, keep nothing between calls
+ * (calls may overlap freely, on any streams, in captured graphs too) and run
+ * on the current device, whose memory the buffers must be.  Outputs must not
+ * overlap inputs except where a call says so; overlaps that the host can see
+ * return SVDQ_ERR_INVALID_ARG.  Row distances (ld*) are in elements and not
+ * negative; that of a single row says nothing.  A call for no rows (M = 0, B
+ * or S = 0) returns SVDQ_OK and does nothing.
  */
 typedef enum {
   SVDQ_BF16 = 0,
